@@ -424,7 +424,8 @@ def _workspace(resa, kind, dims, n):
     """The workspace that a program keeps for calls of one shape."""
     key = (kind, dims.batch, dims.n_q_heads, dims.n_kv_heads, dims.head_dim, dims.dtype, dims.max_len, n)
     if key not in _kept_workspaces:
-        make = resa.alloc_weights_workspace if kind == "weights" else resa.alloc_workspace
+        make = {"weights": resa.alloc_weights_workspace, "kv4": resa.alloc_kv4_workspace,
+                "decode": resa.alloc_workspace}[kind]
         _kept_workspaces[key] = make(dims, n)
     return _kept_workspaces[key]
 
@@ -439,7 +440,7 @@ def _own(s):
         return {"k": s["k_back"], "v": s["v_back"]}
     if op == "kv4":
         dims = resa.dims_kv4(s["kv4"], s["q"])
-        ws = _workspace(resa, "decode", dims, n)
+        ws = _workspace(resa, "kv4", dims, n)
         if "sel" in s:
             resa.attend_blocks_kv4(s["q"], s["kv4"], n, s["sel"], s["scale"], s["out"], ws, lse=s["lse"])
         else:
