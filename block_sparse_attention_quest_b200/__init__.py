@@ -42,7 +42,10 @@ EXPORTED = ("resa_num_selected", "resa_workspace_bytes", "resa_build_desc",
             "resa_decode_dense", "resa_rectify",
             "resa_workspace_status", "resa_status_string", "resa_decode_sparse_noalloc",
             "resa_build_desc_varlen", "resa_decode_sparse_varlen", "resa_decode_dense_varlen",
-            "resa_rectify_varlen", "resa_prefill", "resa_wait_check", "resa_noalloc_status")
+            "resa_rectify_varlen", "resa_prefill", "resa_wait_check", "resa_noalloc_status",
+           "resa_kv4_bytes", "resa_kv4_workspace_bytes", "resa_kv4_quantize",
+           "resa_kv4_dequantize", "resa_decode_dense_kv4", "resa_decode_sparse_kv4",
+           "resa_attend_blocks_kv4")
 
 
 class Dims(ctypes.Structure):
@@ -96,6 +99,25 @@ _lib.resa_rectify_varlen.argtypes = [ctypes.POINTER(Dims), _P, _P, _P, _P, _P, _
 _lib.resa_prefill.restype = ctypes.c_int
 _lib.resa_prefill.argtypes = [ctypes.POINTER(Dims), _P, _P, _P, _P, ctypes.c_int64, ctypes.c_float,
                               _P, _P, ctypes.c_size_t, _P]
+_lib.resa_kv4_bytes.restype = ctypes.c_size_t
+_lib.resa_kv4_bytes.argtypes = [ctypes.POINTER(Dims)]
+_lib.resa_kv4_workspace_bytes.restype = ctypes.c_size_t
+_lib.resa_kv4_workspace_bytes.argtypes = [ctypes.POINTER(Dims), ctypes.c_int64]
+_lib.resa_kv4_quantize.restype = ctypes.c_int
+_lib.resa_kv4_quantize.argtypes = [ctypes.POINTER(Dims), _P, _P, ctypes.c_int64, _P, _P, _P]
+_lib.resa_kv4_dequantize.restype = ctypes.c_int
+_lib.resa_kv4_dequantize.argtypes = [ctypes.POINTER(Dims), _P, ctypes.c_int64, _P, _P, _P, _P]
+_lib.resa_decode_dense_kv4.restype = ctypes.c_int
+_lib.resa_decode_dense_kv4.argtypes = [ctypes.POINTER(Dims), _P, _P, _P, _P, _P, ctypes.c_int64,
+                                       _P, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]
+_lib.resa_decode_sparse_kv4.restype = ctypes.c_int
+_lib.resa_decode_sparse_kv4.argtypes = [ctypes.POINTER(Dims), _P, _P, _P, _P, _P, ctypes.c_int64,
+                                        _P, ctypes.c_double, ctypes.c_int32, ctypes.c_float, _P,
+                                        _P, _P, _P, ctypes.c_size_t, _P]
+_lib.resa_attend_blocks_kv4.restype = ctypes.c_int
+_lib.resa_attend_blocks_kv4.argtypes = [ctypes.POINTER(Dims), _P, _P, ctypes.c_int64, _P,
+                                        ctypes.c_int32, ctypes.c_float, _P, _P, _P,
+                                        ctypes.c_size_t, _P]
 _lib.resa_wait_check.restype = ctypes.c_int
 _lib.resa_wait_check.argtypes = [_P, ctypes.c_int32, ctypes.c_uint32, _P, _P]
 _lib.resa_workspace_status.restype = ctypes.c_int
@@ -298,6 +320,105 @@ def prefill(q, k_cache, v_cache, desc, length: int, softmax_scale: float, out, w
     _check(_lib.resa_prefill(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(desc),
                              int(length), float(softmax_scale), _ptr(out), _ptr(workspace),
                              workspace.numel(), _stream(stream)), "resa_prefill")
+
+
+# ---- the cache in 4 bits: a uint8 tensor [B, H_kv, max_len / 16, record] of
+# records that each hold 16 tokens' keys and values (the format is described in
+# include/resa.h). lens: optional int32 CUDA tensor [batch] of row lengths, with
+# `length` the bound on them.
+
+
+def kv4_record_bytes(head_dim: int) -> int:
+    """Bytes of the record of one 16-token block of one KV head."""
+    return BLOCK * (head_dim + 8 * (head_dim // 64))
+
+
+def dims_kv4(kv4: torch.Tensor, q: torch.Tensor) -> Dims:
+    """Dims of a 4-bit cache serving queries like q [B, H_q, d] (or [.., H_q, d])."""
+    B, H, M, rec = kv4.shape
+    if kv4.dtype != torch.uint8 or rec != kv4_record_bytes(q.shape[-1]):
+        raise ValueError(f"kv4 must be uint8 records of {kv4_record_bytes(q.shape[-1])} bytes")
+    return Dims(B, int(q.shape[-2]), H, int(q.shape[-1]), BLOCK, _dtype_code(q.dtype), M * BLOCK)
+
+
+def alloc_kv4(batch: int, n_kv_heads: int, max_len: int, head_dim: int, device=None) -> torch.Tensor:
+    """Zero-filled 4-bit cache of max_len tokens (a multiple of 16) per row."""
+    return torch.zeros(batch, n_kv_heads, max_len // BLOCK, kv4_record_bytes(head_dim),
+                       dtype=torch.uint8, device=device or "cuda")
+
+
+def kv4_workspace_bytes(dims: Dims, length: int) -> int:
+    n = _lib.resa_kv4_workspace_bytes(ctypes.byref(dims), int(length))
+    if n == 0:
+        raise ResaError(RESA_ERR_INVALID_ARG, "resa_kv4_workspace_bytes")
+    return n
+
+
+def alloc_kv4_workspace(dims: Dims, length: int, device=None) -> torch.Tensor:
+    """Zero-filled workspace (uint8) for the 4-bit decode calls."""
+    return torch.zeros(kv4_workspace_bytes(dims, length), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def _opt_lens(lens):
+    return None if lens is None else _lens(lens)
+
+
+def _kv4_rows(k_cache, v_cache, kv4, n_q_heads: int) -> Dims:
+    B, H, L, d = k_cache.shape
+    if (kv4.dtype != torch.uint8 or tuple(kv4.shape) != (B, H, L // BLOCK, kv4_record_bytes(d))
+            or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype):
+        raise ValueError("kv4 must be the uint8 records of k_cache's and v_cache's shape")
+    return dims_for(k_cache, n_q_heads)
+
+
+def kv4_quantize(k_cache, v_cache, length: int, kv4, n_q_heads: int, lens=None,
+                 stream=None) -> None:
+    """The first `length` tokens of every row into 4-bit records."""
+    dims = _kv4_rows(k_cache, v_cache, kv4, n_q_heads)
+    _check(_lib.resa_kv4_quantize(ctypes.byref(dims), _ptr(k_cache), _ptr(v_cache), int(length),
+                                  _opt_lens(lens), _ptr(kv4), _stream(stream)),
+           "resa_kv4_quantize")
+
+
+def kv4_dequantize(kv4, length: int, k_cache, v_cache, n_q_heads: int, lens=None,
+                   stream=None) -> None:
+    """The values the records stand for, into slots [0, length) of the caches."""
+    dims = _kv4_rows(k_cache, v_cache, kv4, n_q_heads)
+    _check(_lib.resa_kv4_dequantize(ctypes.byref(dims), _ptr(kv4), int(length), _opt_lens(lens),
+                                    _ptr(k_cache), _ptr(v_cache), _stream(stream)),
+           "resa_kv4_dequantize")
+
+
+def decode_dense_kv4(q, k_new, v_new, kv4, desc, length: int, softmax_scale: float, out, workspace,
+                     lse=None, lens=None, stream=None) -> None:
+    """decode_dense on a 4-bit cache (k_new/v_new and desc may be None)."""
+    dims = dims_kv4(kv4, q)
+    _check(_lib.resa_decode_dense_kv4(
+        ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(kv4), _ptr(desc), int(length),
+        _opt_lens(lens), float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel(), _stream(stream)), "resa_decode_dense_kv4")
+
+
+def decode_sparse_kv4(q, k_new, v_new, kv4, desc, length: int, r: float, n_min: int,
+                      softmax_scale: float, out, workspace, lse=None, sel=None, lens=None,
+                      stream=None) -> None:
+    """decode_sparse (with lens: decode_sparse_varlen) on a 4-bit cache."""
+    dims = dims_kv4(kv4, q)
+    _check(_lib.resa_decode_sparse_kv4(
+        ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(kv4), _ptr(desc), int(length),
+        _opt_lens(lens), float(r), int(n_min), float(softmax_scale), _ptr(out), _ptr(lse),
+        _ptr(sel), _ptr(workspace), workspace.numel(), _stream(stream)), "resa_decode_sparse_kv4")
+
+
+def attend_blocks_kv4(q, kv4, length: int, sel, softmax_scale: float, out, workspace, lse=None,
+                      stream=None) -> None:
+    """attend_blocks on a 4-bit cache."""
+    dims = dims_kv4(kv4, q)
+    _check(_lib.resa_attend_blocks_kv4(
+        ctypes.byref(dims), _ptr(q), _ptr(kv4), int(length), _ptr(sel), int(sel.shape[-1]),
+        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+        _stream(stream)), "resa_attend_blocks_kv4")
 
 
 def wait_check(flag, target: int, limit_us: int, workspace, stream=None) -> None:

@@ -591,6 +591,163 @@ int resa_prefill(const resa_dims* dims, const void* q, const void* k_cache, cons
   return cuda_status(launch_rectify_tc(r, static_cast<cudaStream_t>(stream)));
 }
 
+// ---- the 4-bit cache
+
+// Layout of a workspace for the 4-bit decode calls: the control block, the
+// counters and the score and list regions of ws_layout, then the partials of
+// up to two pieces per CTA.
+static WsLayout kv4_layout(const Shape& s, int64_t len) {
+  WsLayout w = ws_layout(s, len, 0);
+  const int64_t rows =
+      2 * static_cast<int64_t>(kv4_ctas(s, blocks_of(len), kKv4MaxCtas)) * s.G;
+  size_t off = w.part_ml;
+  off = align_up(off + static_cast<size_t>(rows) * 2 * sizeof(float));
+  w.part_o = off;
+  w.total = align_up(off + static_cast<size_t>(rows) * s.D * sizeof(float));
+  return w;
+}
+
+size_t resa_kv4_bytes(const resa_dims* dims) {
+  Shape s;
+  if (check_dims(dims, &s) != RESA_OK) return 0;
+  return static_cast<size_t>(s.B) * s.H * s.Mmax * (16 * (s.D + 8 * (s.D / 64)));
+}
+
+size_t resa_kv4_workspace_bytes(const resa_dims* dims, int64_t len) {
+  Shape s;
+  if (check_dims(dims, &s) != RESA_OK || len < 1) return 0;
+  return kv4_layout(s, len).total;
+}
+
+static int check_kv4_rows(const resa_dims* dims, Shape* s, const void* k, const void* v,
+                          const void* kv4, int64_t len, const int32_t* lens) {
+  int rc = check_dims(dims, s);
+  if (rc != RESA_OK) return rc;
+  if (!k || !v || !kv4 || !aligned16(k) || !aligned16(v) || !aligned16(kv4) || len < 1 ||
+      (lens && !lens_ok(lens)))
+    return RESA_ERR_INVALID_ARG;
+  if (len > s->L_max) return RESA_ERR_CAPACITY;
+  return RESA_OK;
+}
+
+int resa_kv4_quantize(const resa_dims* dims, const void* k_cache, const void* v_cache, int64_t len,
+                      const int32_t* lens, void* kv4, void* stream) {
+  Shape s;
+  const int rc = check_kv4_rows(dims, &s, k_cache, v_cache, kv4, len, lens);
+  if (rc != RESA_OK) return rc;
+  return cuda_status(launch_kv4_quantize(s, k_cache, v_cache, kv4, len, lens,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int resa_kv4_dequantize(const resa_dims* dims, const void* kv4, int64_t len, const int32_t* lens,
+                        void* k_cache, void* v_cache, void* stream) {
+  Shape s;
+  const int rc = check_kv4_rows(dims, &s, k_cache, v_cache, kv4, len, lens);
+  if (rc != RESA_OK) return rc;
+  return cuda_status(launch_kv4_dequantize(s, kv4, k_cache, v_cache, len, lens,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+static int check_kv4_decode(const resa_dims* dims, Shape* s, const void* q, const void* k_new,
+                            const void* v_new, const void* kv4, const void* desc, int64_t len,
+                            const int32_t* lens, float softmax_scale, const void* out,
+                            const void* workspace, size_t workspace_bytes) {
+  const int rc = check_dims(dims, s);
+  if (rc != RESA_OK) return rc;
+  if (!q || !kv4 || !out || !workspace || (k_new == nullptr) != (v_new == nullptr) ||
+      !aligned16(q) || !aligned16(kv4) || !aligned16(out) || (desc && !aligned16(desc)) ||
+      (k_new && (!aligned16(k_new) || !aligned16(v_new))) ||
+      (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 || (lens && !lens_ok(lens)) ||
+      len < 1 || !(std::isfinite(softmax_scale) && softmax_scale > 0.f))
+    return RESA_ERR_INVALID_ARG;
+  if (len > s->L_max) return RESA_ERR_CAPACITY;
+  if (workspace_bytes < kv4_layout(*s, len).total) return RESA_ERR_WORKSPACE;
+  return RESA_OK;
+}
+
+static int run_kv4_attention(const Shape& s, const void* q, const void* kv4, int64_t len,
+                             const int32_t* lens, const int32_t* sel, int n_sel, double r,
+                             int n_min, float scale, void* out, float* lse, uint8_t* ws,
+                             int num_sms, cudaStream_t st) {
+  const WsLayout w = kv4_layout(s, len);
+  Kv4Args a{};
+  a.q = q; a.kv4 = kv4; a.sel = sel; a.n_sel = n_sel; a.lens = lens; a.r = r; a.n_min = n_min;
+  a.len = len; a.scale = scale;
+  a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
+  a.counters = reinterpret_cast<int*>(ws + w.counters);
+  a.ctrl = reinterpret_cast<Ctrl*>(ws);
+  a.out = out; a.lse = lse;
+  a.ctas = kv4_ctas(s, sel ? n_sel : blocks_of(len), num_sms);
+  return cuda_status(launch_kv4_attend(s, a, st));
+}
+
+int resa_attend_blocks_kv4(const resa_dims* dims, const void* q, const void* kv4, int64_t len,
+                           const int32_t* sel, int32_t n_sel, float softmax_scale, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  Shape s;
+  const int rc = check_kv4_decode(dims, &s, q, nullptr, nullptr, kv4, nullptr, len, nullptr,
+                                  softmax_scale, out, workspace, workspace_bytes);
+  if (rc != RESA_OK) return rc;
+  if (!sel || n_sel < 1 || n_sel > blocks_of(len)) return RESA_ERR_INVALID_ARG;
+  const int num_sms = device_sms();
+  if (num_sms <= 0) return RESA_ERR_CUDA;
+  return run_kv4_attention(s, q, kv4, len, nullptr, sel, n_sel, 0.0, 0, softmax_scale, out, lse,
+                           static_cast<uint8_t*>(workspace), num_sms,
+                           static_cast<cudaStream_t>(stream));
+}
+
+int resa_decode_dense_kv4(const resa_dims* dims, const void* q, const void* k_new,
+                          const void* v_new, void* kv4, void* desc, int64_t len,
+                          const int32_t* lens, float softmax_scale, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  Shape s;
+  const int rc = check_kv4_decode(dims, &s, q, k_new, v_new, kv4, desc, len, lens, softmax_scale,
+                                  out, workspace, workspace_bytes);
+  if (rc != RESA_OK) return rc;
+  const int num_sms = device_sms();
+  if (num_sms <= 0) return RESA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (k_new &&
+      launch_kv4_append(s, k_new, v_new, kv4, desc, len, lens, st) != cudaSuccess)
+    return RESA_ERR_CUDA;
+  return run_kv4_attention(s, q, kv4, len, lens, nullptr, 0, 0.0, 0, softmax_scale, out, lse,
+                           static_cast<uint8_t*>(workspace), num_sms, st);
+}
+
+int resa_decode_sparse_kv4(const resa_dims* dims, const void* q, const void* k_new,
+                           const void* v_new, void* kv4, void* desc, int64_t len,
+                           const int32_t* lens, double r, int32_t n_min, float softmax_scale,
+                           void* out, float* lse, int32_t* sel, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  Shape s;
+  const int rc = check_kv4_decode(dims, &s, q, k_new, v_new, kv4, desc, len, lens, softmax_scale,
+                                  out, workspace, workspace_bytes);
+  if (rc != RESA_OK) return rc;
+  if (!desc || !(r > 0.0 && r <= 1.0) || n_min < 1) return RESA_ERR_INVALID_ARG;
+  if (blocks_of(len) > 262144) return RESA_ERR_UNSUPPORTED;
+  const int num_sms = device_sms();
+  if (num_sms <= 0) return RESA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const WsLayout w = kv4_layout(s, len);
+  float* scores = reinterpret_cast<float*>(ws + w.scores);
+  int32_t* selp = sel ? sel : reinterpret_cast<int32_t*>(ws + w.sel);
+  const int M = static_cast<int>(blocks_of(len));
+  const int n = resa_num_selected(len, 16, r, n_min);
+  if (k_new &&
+      launch_kv4_append(s, k_new, v_new, kv4, desc, len, lens, st) != cudaSuccess)
+    return RESA_ERR_CUDA;
+  // (the scores never read block M-1, the one the append touches)
+  if (launch_score(s, q, desc, scores, nullptr, nullptr, nullptr, nullptr, nullptr, len, num_sms,
+                   st, lens, reinterpret_cast<Ctrl*>(ws)) != cudaSuccess)
+    return RESA_ERR_CUDA;
+  if (launch_select(s, scores, selp, M, n, st, lens, len, r, n_min) != cudaSuccess)
+    return RESA_ERR_CUDA;
+  return run_kv4_attention(s, q, kv4, len, lens, selp, n, r, n_min, softmax_scale, out, lse, ws,
+                           num_sms, st);
+}
+
 int resa_wait_check(const int32_t* flag, int32_t target, uint32_t limit_us, void* workspace,
                     void* stream) {
   if (!flag || (reinterpret_cast<uintptr_t>(flag) & 3u) != 0 || !workspace ||

@@ -133,6 +133,38 @@ struct RectArgs {
 cudaError_t launch_rectify_tc(const RectArgs& r, cudaStream_t st);
 int attend_ctas_per_sm(const Shape& s);
 
+// 4-bit cache (kv4.cuh) --------------------------------------------------------
+// rows of a cache to records and back; lens: optional per-row lengths [B]
+cudaError_t launch_kv4_quantize(const Shape& s, const void* k, const void* v, void* kv4,
+                                int64_t len, const int32_t* lens, cudaStream_t st);
+cudaError_t launch_kv4_dequantize(const Shape& s, const void* kv4, void* k, void* v, int64_t len,
+                                  const int32_t* lens, cudaStream_t st);
+// token len - 1 into its record and (desc != nullptr) its block's descriptor
+cudaError_t launch_kv4_append(const Shape& s, const void* k_new, const void* v_new, void* kv4,
+                              void* desc, int64_t len, const int32_t* lens, cudaStream_t st);
+struct Kv4Args {
+  const void* q;
+  const void* kv4;
+  const int32_t* sel;     // [B][H][n_sel] or nullptr (every block)
+  int n_sel;
+  const int32_t* lens;    // optional per-row lengths [B]; with sel, row b lists
+  double r;               // Eq. 5's count for its own length (r, n_min)
+  int n_min;
+  int64_t len;
+  float scale;
+  float* part_o;          // [2 * ctas][G][D]
+  float* part_ml;         // [2 * ctas][G][2]
+  int* counters;          // [B * H], zero between calls
+  Ctrl* ctrl;
+  void* out;
+  float* lse;
+  int ctas;               // kv4_ctas
+};
+cudaError_t launch_kv4_attend(const Shape& s, const Kv4Args& a, cudaStream_t st);
+constexpr int kKv4MaxCtas = 512;
+// CTAs of a launch over at most blocks_bound blocks per (row, KV head)
+int kv4_ctas(const Shape& s, int64_t blocks_bound, int num_sms);
+
 // bounded wait of one thread until *flag >= target (failure-detection check)
 cudaError_t launch_wait_check(const int* flag, int target, unsigned long long limit_ns,
                               Ctrl* ctrl, cudaStream_t st);

@@ -290,6 +290,78 @@ RESA_API int resa_rectify_varlen(const resa_dims* dims, const void* q_f, const v
                                  int32_t f, float softmax_scale, void* out_f, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* ---- the cache in 4 bits ----
+ * The pages run their INT4 series on the same method; the format below is this
+ * library's. Sixteen tokens (one block) of one KV head form one record of
+ * 16 * (d + 8 d / 64) bytes (2304 for d = 128 where bf16 keys and values take
+ * 8192), and the cache is
+ *     kv4   [batch][n_kv_heads][max_len/16][record]   bytes, 16-byte aligned
+ * of resa_kv4_bytes() bytes.
+ *  - A group of 64 channels of a token's key or value is held as
+ *    x = zero + scale * code: scale = bf16((max - min) * fp32(1/15)), zero =
+ *    bf16(min), code = rint((x - zero) / scale) in 0..15 (0 where the scale is
+ *    0), in fp32 arithmetic with halves to the even code.
+ *  - Inside a record: key codes, value codes, then {key scale, key zero, value
+ *    scale, value zero} in bf16 per token and group:
+ *      key of token 8h + r, channel 64g + 16c + 8j + i: nibble i (lowest
+ *        first) of 32-bit word [g][r][c][2h + j];
+ *      value of token 8h + 2c + o, channel 64g + 16m + 8e + r: nibble
+ *        e + 2h + 4o of word [g][r][c][m];
+ *      scales of token 8h + r, group g: [r][h][g][4].
+ *  - Values must be finite and below 2^60 in magnitude, queries below 2^60;
+ *    others give unspecified outputs in their own row (NaN and infinity are
+ *    not carried through the format).
+ *  - dims.dtype is the type of q, k, v, desc and out; the records are the same
+ *    for both types.
+ *  - lens is optional in these calls (NULL: every row has `len` tokens); with
+ *    lens (DEVICE int32 [batch]) `len` is the bound on its entries, as in the
+ *    *_varlen calls.
+ *  - Descriptors stay those of the unquantised keys: build them before the
+ *    cache is dropped; the decode calls merge each appended key into them.
+ * Rectification has no 4-bit form: it rewrites a window of exact entries. */
+
+/* Bytes of a 4-bit cache of these dims; 0 for invalid dims. */
+RESA_API size_t resa_kv4_bytes(const resa_dims* dims);
+
+/* Workspace bytes that suffice for the three decode calls below at any length
+ * up to `len`; 0 for invalid dims or len < 1. */
+RESA_API size_t resa_kv4_workspace_bytes(const resa_dims* dims, int64_t len);
+
+/* The first `len` (lens[b]) tokens of every row of k_cache and v_cache into
+ * records; slots past a row's end in its last record are zero, later records
+ * are not written. */
+RESA_API int resa_kv4_quantize(const resa_dims* dims, const void* k_cache, const void* v_cache,
+                               int64_t len, const int32_t* lens, void* kv4, void* stream);
+
+/* The values the records stand for, zero + scale * code in fp32 rounded once
+ * to dims.dtype, into slots [0, len) (lens[b]) of k_cache and v_cache. */
+RESA_API int resa_kv4_dequantize(const resa_dims* dims, const void* kv4, int64_t len,
+                                 const int32_t* lens, void* k_cache, void* v_cache, void* stream);
+
+/* resa_decode_dense on a 4-bit cache: if k_new != NULL, k_new/v_new are
+ * quantised into slot len-1 (and k_new merged into its block's descriptor when
+ * desc != NULL); then attention over the values the records of every token
+ * < len stand for. */
+RESA_API int resa_decode_dense_kv4(const resa_dims* dims, const void* q, const void* k_new,
+                                   const void* v_new, void* kv4, void* desc, int64_t len,
+                                   const int32_t* lens, float softmax_scale, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* resa_decode_sparse on a 4-bit cache: append as above, scores from the
+ * descriptors, top-n selection (`sel` as in resa_decode_sparse and, with lens,
+ * resa_decode_sparse_varlen), attention over the selected records. */
+RESA_API int resa_decode_sparse_kv4(const resa_dims* dims, const void* q, const void* k_new,
+                                    const void* v_new, void* kv4, void* desc, int64_t len,
+                                    const int32_t* lens, double r, int32_t n_min,
+                                    float softmax_scale, void* out, float* lse, int32_t* sel,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* resa_attend_blocks on a 4-bit cache. */
+RESA_API int resa_attend_blocks_kv4(const resa_dims* dims, const void* q, const void* kv4,
+                                    int64_t len, const int32_t* sel, int32_t n_sel,
+                                    float softmax_scale, void* out, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 /* Failure-detection check of the device-side bounded wait (no counterpart in
  * the method): one thread waits until the device int32 *flag >= target, as
  * the one-launch decode kernel's group barrier waits on its arrival counter,
