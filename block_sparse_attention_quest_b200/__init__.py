@@ -45,7 +45,8 @@ EXPORTED = ("resa_num_selected", "resa_workspace_bytes", "resa_build_desc",
             "resa_rectify_varlen", "resa_prefill", "resa_wait_check", "resa_noalloc_status",
            "resa_kv4_bytes", "resa_kv4_workspace_bytes", "resa_kv4_quantize",
            "resa_kv4_dequantize", "resa_decode_dense_kv4", "resa_decode_sparse_kv4",
-           "resa_attend_blocks_kv4")
+           "resa_attend_blocks_kv4", "resa_weights_workspace_bytes",
+           "resa_decode_dense_weights", "resa_evict")
 
 
 class Dims(ctypes.Structure):
@@ -118,6 +119,16 @@ _lib.resa_attend_blocks_kv4.restype = ctypes.c_int
 _lib.resa_attend_blocks_kv4.argtypes = [ctypes.POINTER(Dims), _P, _P, ctypes.c_int64, _P,
                                         ctypes.c_int32, ctypes.c_float, _P, _P, _P,
                                         ctypes.c_size_t, _P]
+_lib.resa_weights_workspace_bytes.restype = ctypes.c_size_t
+_lib.resa_weights_workspace_bytes.argtypes = [ctypes.POINTER(Dims), ctypes.c_int64]
+_lib.resa_decode_dense_weights.restype = ctypes.c_int
+_lib.resa_decode_dense_weights.argtypes = [ctypes.POINTER(Dims), _P, _P, _P, _P, _P, _P, _P,
+                                           ctypes.c_int64, _P, ctypes.c_float, _P, _P, _P,
+                                           ctypes.c_size_t, _P]
+_lib.resa_evict.restype = ctypes.c_int
+_lib.resa_evict.argtypes = [ctypes.POINTER(Dims), _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int32,
+                            ctypes.c_int32, ctypes.c_int64, _P, _P, _P, _P, _P, _P,
+                            ctypes.c_size_t, _P]
 _lib.resa_wait_check.restype = ctypes.c_int
 _lib.resa_wait_check.argtypes = [_P, ctypes.c_int32, ctypes.c_uint32, _P, _P]
 _lib.resa_workspace_status.restype = ctypes.c_int
@@ -322,6 +333,65 @@ def prefill(q, k_cache, v_cache, desc, length: int, softmax_scale: float, out, w
                              workspace.numel(), _stream(stream)), "resa_prefill")
 
 
+# ---- attention weights (float32 [B, H_kv, max_len] running sums) and eviction
+
+
+def _opt_lens(lens):
+    return None if lens is None else _lens(lens)
+
+
+def _weights(weights, k_cache):
+    if weights.dtype != torch.float32 or tuple(weights.shape) != tuple(k_cache.shape[:3]):
+        raise ValueError("weights must be float32 [batch, n_kv_heads, max_len]")
+    return _ptr(weights)
+
+
+def weights_workspace_bytes(dims: Dims, length: int) -> int:
+    n = _lib.resa_weights_workspace_bytes(ctypes.byref(dims), int(length))
+    if n == 0:
+        raise ResaError(RESA_ERR_INVALID_ARG, "resa_weights_workspace_bytes")
+    return n
+
+
+def alloc_weights_workspace(dims: Dims, length: int, device=None) -> torch.Tensor:
+    """Zero-filled workspace (uint8) for decode_dense_weights."""
+    return torch.zeros(weights_workspace_bytes(dims, length), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def decode_dense_weights(q, k_new, v_new, k_cache, v_cache, desc, weights, length: int,
+                         softmax_scale: float, out, lse, workspace, lens=None,
+                         stream=None) -> None:
+    """decode_dense that also adds every token's attention weight to `weights`
+    (desc and lse may be None)."""
+    dims = dims_for(k_cache, q.shape[1])
+    _check(_lib.resa_decode_dense_weights(
+        ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+        _ptr(desc), _weights(weights, k_cache), int(length), _opt_lens(lens),
+        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+        _stream(stream)), "resa_decode_dense_weights")
+
+
+def evict(k_cache, v_cache, weights, length: int, budget: int, n_recent: int, k_out, v_out,
+          desc_out, weights_out, kept, n_q_heads: int, workspace, lens=None, stream=None) -> None:
+    """Cut every (row, KV head) to its newest n_recent tokens and the
+    budget - n_recent others of the largest weight (desc_out and weights_out
+    may be None; kept: int32 [B, H_kv, budget])."""
+    dims = dims_for(k_cache, n_q_heads)
+    B, H, Lo, d = k_out.shape
+    if (tuple(k_out.shape) != (k_cache.shape[0], k_cache.shape[1], Lo, k_cache.shape[3])
+            or v_out.shape != k_out.shape or k_out.dtype != k_cache.dtype
+            or v_out.dtype != k_cache.dtype):
+        raise ValueError("k_out and v_out must be [batch, n_kv_heads, out_max_len, head_dim]")
+    if kept.dtype != torch.int32 or tuple(kept.shape) != (B, H, budget):
+        raise ValueError("kept must be int32 [batch, n_kv_heads, budget]")
+    _check(_lib.resa_evict(
+        ctypes.byref(dims), _ptr(k_cache), _ptr(v_cache), _weights(weights, k_cache), int(length),
+        _opt_lens(lens), int(budget), int(n_recent), Lo, _ptr(k_out), _ptr(v_out), _ptr(desc_out),
+        None if weights_out is None else _weights(weights_out, k_out), _ptr(kept),
+        _ptr(workspace), workspace.numel(), _stream(stream)), "resa_evict")
+
+
 # ---- the cache in 4 bits: a uint8 tensor [B, H_kv, max_len / 16, record] of
 # records that each hold 16 tokens' keys and values (the format is described in
 # include/resa.h). lens: optional int32 CUDA tensor [batch] of row lengths, with
@@ -358,10 +428,6 @@ def alloc_kv4_workspace(dims: Dims, length: int, device=None) -> torch.Tensor:
     """Zero-filled workspace (uint8) for the 4-bit decode calls."""
     return torch.zeros(kv4_workspace_bytes(dims, length), dtype=torch.uint8,
                        device=device or "cuda")
-
-
-def _opt_lens(lens):
-    return None if lens is None else _lens(lens)
 
 
 def _kv4_rows(k_cache, v_cache, kv4, n_q_heads: int) -> Dims:

@@ -227,7 +227,8 @@ int run_attention(const Shape& s, const void* q, int R, int64_t len0, const int3
                   float scale, const void* k, const void* v, void* out, float* lse, uint8_t* ws,
                   const WsLayout& w, int num_sms, cudaStream_t st, bool pdl = false,
                   const int32_t* lens = nullptr, double r = 0.0, int n_min = 0,
-                  const int32_t* windows = nullptr) {
+                  const int32_t* windows = nullptr, float* logits = nullptr,
+                  float* ml = nullptr) {
   const int64_t min_blocks = sel ? n_sel : blocks_of(len0);
   const int S = splits_for(s.B * s.H * R, min_blocks, num_sms, s);
   AttnArgs a{};
@@ -241,6 +242,7 @@ int run_attention(const Shape& s, const void* q, int R, int64_t len0, const int3
   a.k = k; a.v = v;
   a.pdl = pdl;
   a.lens = lens; a.windows = windows; a.r = r; a.n_min = n_min;
+  a.logits = logits; a.ml = ml; a.logit_stride = blocks_of(len0) * 16;
   CUtensorMap tk, tv;
   if (s.bf16) {
     if (!make_cache_map(&tk, k, s) || !make_cache_map(&tv, v, s)) return RESA_ERR_CUDA;
@@ -589,6 +591,102 @@ int resa_prefill(const resa_dims* dims, const void* q, const void* k_cache, cons
     return RESA_ERR_CUDA;
   r.tm_q = &tq; r.tm_k = &tk; r.tm_v = &tv;
   return cuda_status(launch_rectify_tc(r, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- attention weights and eviction
+
+// ws_layout, then every token's logits and each head's (max, sum)
+struct WeightsLayout {
+  size_t logits, ml, total;
+};
+static WeightsLayout weights_layout(const Shape& s, int64_t len) {
+  WeightsLayout w{};
+  w.ml = ws_layout(s, len, 0).total;
+  w.logits = align_up(w.ml + static_cast<size_t>(s.B) * s.Hq * 2 * sizeof(float));
+  w.total = align_up(w.logits + static_cast<size_t>(s.B) * s.Hq * blocks_of(len) * 16 * sizeof(float));
+  return w;
+}
+
+size_t resa_weights_workspace_bytes(const resa_dims* dims, int64_t len) {
+  Shape s;
+  if (check_dims(dims, &s) != RESA_OK || len < 1) return 0;
+  return weights_layout(s, len).total;
+}
+
+int resa_decode_dense_weights(const resa_dims* dims, const void* q, const void* k_new,
+                              const void* v_new, void* k_cache, void* v_cache, void* desc,
+                              float* weights, int64_t len, const int32_t* lens,
+                              float softmax_scale, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  Shape s;
+  int rc = check_decode_common(dims, &s, q, k_new, v_new, k_cache, v_cache, len, out, workspace,
+                               workspace_bytes, 0);
+  if (rc != RESA_OK) return rc;
+  if (!weights || !aligned16(weights) || (desc && !aligned16(desc)) || (lens && !lens_ok(lens)) ||
+      !(std::isfinite(softmax_scale) && softmax_scale > 0.f))
+    return RESA_ERR_INVALID_ARG;
+  const WeightsLayout wl = weights_layout(s, len);
+  if (workspace_bytes < wl.total) return RESA_ERR_WORKSPACE;
+  const int num_sms = device_sms();
+  if (num_sms <= 0) return RESA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const WsLayout w = ws_layout(s, len, 0);
+  float* logits = reinterpret_cast<float*>(ws + wl.logits);
+  float* ml = reinterpret_cast<float*>(ws + wl.ml);
+  if (k_new &&
+      launch_append(s, k_new, v_new, k_cache, v_cache, desc, len, st, lens) != cudaSuccess)
+    return RESA_ERR_CUDA;
+  rc = run_attention(s, q, 1, len, nullptr, 0, softmax_scale, k_cache, v_cache, out, lse, ws, w,
+                     num_sms, st, false, lens, 0.0, 0, nullptr, logits, ml);
+  if (rc != RESA_OK) return rc;
+  return cuda_status(launch_add_weights(s, logits, ml, weights, len, lens, k_new != nullptr, st));
+}
+
+// whether [a, a + n) and [b, b + m) share a byte
+static bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + m && y < x + n;
+}
+
+int resa_evict(const resa_dims* dims, const void* k_cache, const void* v_cache,
+               const float* weights, int64_t len, const int32_t* lens, int32_t budget,
+               int32_t n_recent, int64_t out_max_len, void* k_out, void* v_out, void* desc_out,
+               float* weights_out, int32_t* kept, void* workspace, size_t workspace_bytes,
+               void* stream) {
+  Shape s;
+  int rc = check_decode_common(dims, &s, k_cache, nullptr, nullptr, k_cache, v_cache, len, k_out,
+                               workspace, workspace_bytes, 0);
+  if (rc != RESA_OK) return rc;
+  if (!weights || !v_out || !kept || !aligned16(weights) || !aligned16(v_out) ||
+      (desc_out && !aligned16(desc_out)) || (reinterpret_cast<uintptr_t>(kept) & 3u) != 0 ||
+      (weights_out && (reinterpret_cast<uintptr_t>(weights_out) & 3u) != 0) ||
+      (lens && !lens_ok(lens)) || budget < 1 || n_recent < 0 || n_recent > budget ||
+      out_max_len < 16 || out_max_len % 16 != 0)
+    return RESA_ERR_INVALID_ARG;
+  if (budget > out_max_len) return RESA_ERR_CAPACITY;
+  if (len > 2147483647LL - 65536) return RESA_ERR_UNSUPPORTED;
+  // rows are read while others are written: the outputs are other memory
+  const size_t e = s.bf16 ? 2 : 4, rows = static_cast<size_t>(s.B) * s.H;
+  const size_t in_kv = rows * static_cast<size_t>(s.L_max) * s.D * e;
+  const size_t in_w = rows * static_cast<size_t>(s.L_max) * sizeof(float);
+  const size_t out_kv = rows * static_cast<size_t>(out_max_len) * s.D * e;
+  const size_t out_w = rows * static_cast<size_t>(out_max_len) * sizeof(float);
+  const size_t out_d = out_kv / 8, out_i = rows * static_cast<size_t>(budget) * sizeof(int32_t);
+  const struct { const void* p; size_t n; } in[3] = {{k_cache, in_kv}, {v_cache, in_kv}, {weights, in_w}},
+      res[5] = {{k_out, out_kv}, {v_out, out_kv}, {weights_out, out_w}, {desc_out, out_d}, {kept, out_i}};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 3; ++j)
+      if (overlap(in[j].p, in[j].n, res[i].p, res[i].n)) return RESA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(res[j].p, res[j].n, res[i].p, res[i].n)) return RESA_ERR_INVALID_ARG;
+  }
+  EvictArgs a{};
+  a.k = k_cache; a.v = v_cache; a.weights = weights; a.len = len; a.lens = lens;
+  a.budget = budget; a.recent = n_recent; a.L_out = out_max_len; a.k_out = k_out; a.v_out = v_out;
+  a.desc_out = desc_out; a.weights_out = weights_out; a.kept = kept;
+  a.ctrl = reinterpret_cast<Ctrl*>(workspace);
+  return cuda_status(launch_evict(s, a, static_cast<cudaStream_t>(stream)));
 }
 
 // ---- the 4-bit cache

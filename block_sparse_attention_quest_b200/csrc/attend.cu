@@ -71,8 +71,29 @@ __device__ __forceinline__ IdCache load_ids(const int32_t* selp, int i0, int i1,
   return c;
 }
 
+// Stores the logits of the valid tokens of one (row, KV head): [token][G].
+struct StoreLogits {
+  float* base;
+  int64_t len;
+  int G;
+  __device__ __forceinline__ void operator()(int64_t t, float s0, float s1, float s2,
+                                             float s3) const {
+    const int h = 2 * (threadIdx.x & 3);
+    if (h >= G) return;
+    float* p = base + t * G + h;
+    if ((G & 1) == 0) {
+      if (t < len) *reinterpret_cast<float2*>(p) = make_float2(s0, s1);
+      if (t + 8 < len) *reinterpret_cast<float2*>(p + 8 * G) = make_float2(s2, s3);
+    } else {
+      const bool two = h + 1 < G;
+      if (t < len) { p[0] = s0; if (two) p[1] = s1; }
+      if (t + 8 < len) { p[8 * G] = s2; if (two) p[8 * G + 1] = s3; }
+    }
+  }
+};
+
 // ---------------------------------------------------------------------- bf16
-template <int D, int NW, int STAGES>
+template <int D, int NW, int STAGES, bool KEEP = false>
 __global__ void __launch_bounds__(NW * 32) attend_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
                                                               const __grid_constant__ CUtensorMap tmV,
                                                               AttnK a) {
@@ -120,18 +141,26 @@ __global__ void __launch_bounds__(NW * 32) attend_bf16_kernel(const __grid_const
   };
   float o[KT][4];
   float m0, m1, l0, l1;
-  const bool ok = stream_bf16<D, NW, STAGES>(&tmK, &tmV, tiles, bars, block_of, my_count, row_base,
-                                             len_r, qb, a.scale_log2, a.ctrl, o, m0, m1, l0, l1);
+  bool ok;
+  if constexpr (KEEP) {
+    const StoreLogits keep{a.logits + (static_cast<int64_t>(b) * a.H + g) * a.logit_stride * a.G,
+                           len_r, a.G};
+    ok = stream_bf16<D, NW, STAGES>(&tmK, &tmV, tiles, bars, block_of, my_count, row_base, len_r,
+                                    qb, a.scale_log2, a.ctrl, o, m0, m1, l0, l1, keep);
+  } else {
+    ok = stream_bf16<D, NW, STAGES>(&tmK, &tmV, tiles, bars, block_of, my_count, row_base, len_r,
+                                    qb, a.scale_log2, a.ctrl, o, m0, m1, l0, l1);
+  }
   // The next kernel in the stream may launch once every CTA has streamed its
   // blocks (whatever it reads from this kernel it reads after its own
   // dependency wait); launched earlier its prologue would compete with the
   // stream, launched here it overlaps the merge tail.
   grid_launch_dependents();
-  finish_bf16<D, NW, STAGES>(a, tiles, ok, o, m0, m1, l0, l1, br, g, s_idx);
+  finish_bf16<D, NW, STAGES, KEEP>(a, tiles, ok, o, m0, m1, l0, l1, br, g, s_idx);
 }
 
 // ---------------------------------------------------------------------- fp32
-template <int D, int NW>
+template <int D, int NW, bool KEEP = false>
 __global__ void __launch_bounds__(NW * 32) attend_f32_kernel(AttnK a) {
   constexpr int P = D + 1;                    // padded row (conflict-free column reads)
   constexpr int CPL = D / 32;                 // output channels per lane
@@ -202,6 +231,11 @@ __global__ void __launch_bounds__(NW * 32) attend_f32_kernel(AttnK a) {
           part = fmaf(sq[h * D + c], Ks[t * P + c], part);
         part += __shfl_xor_sync(0xffffffffu, part, 16);
         const float z = valid ? part * a.scale_log2 : -INFINITY;
+        if constexpr (KEEP) {
+          if (valid && half == 0)
+            a.logits[((static_cast<int64_t>(b) * a.H + g) * a.logit_stride +
+                      static_cast<int64_t>(j) * kBlock + t) * a.G + h] = z;
+        }
         float mx = z;
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -240,14 +274,14 @@ __global__ void __launch_bounds__(NW * 32) attend_f32_kernel(AttnK a) {
     }
   }
   __syncthreads();
-  cta_finish<float, D, NW>(a, sm, br, g, s_idx);
+  cta_finish<float, D, NW, KEEP>(a, sm, br, g, s_idx);
 }
 
 // ---------------------------------------------------------------------- launch
 constexpr int kNW = 8;        // warps per CTA (one CTA per SM for bf16)
 constexpr int kStages = 2;    // tiles in flight per warp (3: no faster, more shared memory)
 
-template <int D>
+template <int D, bool KEEP>
 static cudaError_t attend_bf16_t(const Shape& s, const AttnK& k, const AttnArgs& a,
                                  cudaStream_t st) {
   using Cfg = Bf16Cfg<D, kNW, kStages>;
@@ -255,7 +289,7 @@ static cudaError_t attend_bf16_t(const Shape& s, const AttnK& k, const AttnArgs&
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(attend_bf16_kernel<D, kNW, kStages>,
+    cudaError_t e = cudaFuncSetAttribute(attend_bf16_kernel<D, kNW, kStages, KEEP>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
@@ -270,10 +304,10 @@ static cudaError_t attend_bf16_t(const Shape& s, const AttnK& k, const AttnArgs&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attend_bf16_kernel<D, kNW, kStages>, *a.tm_k, *a.tm_v, k);
+  return cudaLaunchKernelEx(&cfg, attend_bf16_kernel<D, kNW, kStages, KEEP>, *a.tm_k, *a.tm_v, k);
 }
 
-template <int D>
+template <int D, bool KEEP>
 static cudaError_t attend_f32_t(const Shape& s, const AttnK& k, const AttnArgs& a,
                                 cudaStream_t st) {
   const size_t tiles = static_cast<size_t>(kNW) * 2 * 16 * (D + 1);
@@ -283,7 +317,7 @@ static cudaError_t attend_f32_t(const Shape& s, const AttnK& k, const AttnArgs& 
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<D, kNW>,
+    cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<D, kNW, KEEP>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -299,7 +333,7 @@ static cudaError_t attend_f32_t(const Shape& s, const AttnK& k, const AttnArgs& 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attend_f32_kernel<D, kNW>, k);
+  return cudaLaunchKernelEx(&cfg, attend_f32_kernel<D, kNW, KEEP>, k);
 }
 
 int attend_ctas_per_sm(const Shape& s) { return s.bf16 ? 1 : 2; }
@@ -312,8 +346,15 @@ cudaError_t launch_attend(const Shape& s, const AttnArgs& a, cudaStream_t st) {
   k.G = s.G; k.n_sel = a.n_sel; k.S = a.S;
   k.lens = a.lens; k.windows = a.windows; k.r = a.r; k.n_min = a.n_min;
   k.scale_log2 = a.scale * 1.4426950408889634f;
-  if (s.bf16) return s.D == 128 ? attend_bf16_t<128>(s, k, a, st) : attend_bf16_t<64>(s, k, a, st);
-  return s.D == 128 ? attend_f32_t<128>(s, k, a, st) : attend_f32_t<64>(s, k, a, st);
+  k.logits = a.logits; k.ml = a.ml; k.logit_stride = a.logit_stride;
+  if (a.logits != nullptr) {
+    if (s.bf16)
+      return s.D == 128 ? attend_bf16_t<128, true>(s, k, a, st) : attend_bf16_t<64, true>(s, k, a, st);
+    return s.D == 128 ? attend_f32_t<128, true>(s, k, a, st) : attend_f32_t<64, true>(s, k, a, st);
+  }
+  if (s.bf16)
+    return s.D == 128 ? attend_bf16_t<128, false>(s, k, a, st) : attend_bf16_t<64, false>(s, k, a, st);
+  return s.D == 128 ? attend_f32_t<128, false>(s, k, a, st) : attend_f32_t<64, false>(s, k, a, st);
 }
 
 }  // namespace resa

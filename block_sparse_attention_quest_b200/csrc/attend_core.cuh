@@ -32,6 +32,17 @@ struct AttnK {
   int n_min;
   int R, Hq, H, G, n_sel, S;
   float scale_log2;
+  // weight-keeping decode (R = 1, no list) only: every token's logits in
+  // log2 units, [B][H][logit_stride][G], and each head's (max, sum) [B][Hq][2]
+  float* logits;
+  float* ml;
+  int64_t logit_stride;
+};
+
+// What a streaming loop does with the logits of a block besides the softmax:
+// nothing here, a store in the weight-keeping decode.
+struct NoLogits {
+  __device__ __forceinline__ void operator()(int64_t, float, float, float, float) const {}
 };
 
 // Row stride (floats) of the per-warp outputs in shared memory: 4 floats of
@@ -48,7 +59,8 @@ __host__ __device__ constexpr int merge_floats(int D, int NW) { return NW * 8 * 
 // sm must hold merge_floats(D, NW) floats; it is reused by the final merge.
 // Returns true in the CTA that wrote the group's final output (the only CTA
 // when S == 1, else the last one to arrive); false in the others.
-template <typename T, int D, int NW>
+// KEEP_ML also leaves each head's (max in log2 units, sum) in a.ml.
+template <typename T, int D, int NW, bool KEEP_ML = false>
 __device__ __forceinline__ bool cta_finish(const AttnK& a, float* sm, int br, int g, int s_idx) {
   constexpr int OR = merge_row(D);
   float* sm_o = sm;                       // [NW][8][OR]
@@ -57,6 +69,12 @@ __device__ __forceinline__ bool cta_finish(const AttnK& a, float* sm, int br, in
   __shared__ int s_last;
   T* out = static_cast<T*>(a.out);
   const int64_t head0 = static_cast<int64_t>(br) * a.Hq + g * a.G;
+  auto keep_ml = [&](int h, float m, float l) {
+    if constexpr (KEEP_ML) {
+      a.ml[(head0 + h) * 2] = m;
+      a.ml[(head0 + h) * 2 + 1] = l;
+    }
+  };
   constexpr int NT = NW * 32;
   constexpr int HALF = D / 2;
   // One output channel pair (c, c + HALF) of one head per thread when the
@@ -82,6 +100,7 @@ __device__ __forceinline__ bool cta_finish(const AttnK& a, float* sm, int br, in
       out[(head0 + h) * D + ch] = Dt<T>::from_f(o0 / l);
       if (paired) out[(head0 + h) * D + ch + HALF] = Dt<T>::from_f(o1 / l);
       if (a.lse != nullptr && ch == 0) a.lse[head0 + h] = (mstar + log2f(l)) * 0.69314718055994531f;
+      if (ch == 0) keep_ml(h, mstar, l);
     } else {
       const int64_t row = (head0 + h) * a.S + s_idx;
       a.part_o[row * D + ch] = o0;
@@ -147,6 +166,7 @@ __device__ __forceinline__ bool cta_finish(const AttnK& a, float* sm, int br, in
           if (u < a.S) o = fmaf(w_s[u * 8 + h], x[it][u], o);
         out[(head0 + h) * D + ch] = Dt<T>::from_f(o / l_h[h]);
         if (a.lse != nullptr && ch == 0) a.lse[head0 + h] = (m_h[h] + log2f(l_h[h])) * 0.69314718055994531f;
+        if (ch == 0) keep_ml(h, m_h[h], l_h[h]);
       }
     }
     if (threadIdx.x == 0) *counter = 0;
@@ -184,6 +204,7 @@ __device__ __forceinline__ bool cta_finish(const AttnK& a, float* sm, int br, in
     }
     out[(head0 + h) * D + ch] = Dt<T>::from_f(run_o / run_l);
     if (a.lse != nullptr && ch == 0) a.lse[head0 + h] = (run_m + log2f(run_l)) * 0.69314718055994531f;
+    if (ch == 0) keep_ml(h, run_m, run_l);
   }
   if (threadIdx.x == 0) *counter = 0;
   return true;
@@ -208,13 +229,14 @@ struct Bf16Cfg {
 // bf16. Tokens at or past len_r are masked and their V rows zeroed. Returns
 // false (time-out raised) when a tile did not arrive in time; the copies
 // still in flight are drained before returning.
-template <int D, int NW, int STAGES, typename BlockOf>
+template <int D, int NW, int STAGES, typename BlockOf, typename Keep = NoLogits>
 __device__ __forceinline__ bool stream_bf16(const CUtensorMap* tmK, const CUtensorMap* tmV,
                                             uint8_t* tiles, uint64_t (*bars)[STAGES],
                                             BlockOf block_of, int my_count, int64_t row_base,
                                             int64_t len_r, const uint32_t (&qb)[D / 16][2],
                                             float sl2, Ctrl* ctrl, float (&o)[D / 16][4],
-                                            float& m0, float& m1, float& l0, float& l1) {
+                                            float& m0, float& m1, float& l0, float& l1,
+                                            Keep keep = Keep{}) {
   using Cfg = Bf16Cfg<D, NW, STAGES>;
   constexpr int KT = D / 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -286,6 +308,7 @@ __device__ __forceinline__ bool stream_bf16(const CUtensorMap* tmK, const CUtens
     // sacc: (token gq, head 2cq), (gq, 2cq+1), (gq+8, 2cq), (gq+8, 2cq+1)
     const int64_t t_lo = static_cast<int64_t>(j) * kBlock + gq;
     float s0 = sacc[0] * sl2, s1 = sacc[1] * sl2, s2 = sacc[2] * sl2, s3 = sacc[3] * sl2;
+    keep(t_lo, s0, s1, s2, s3);
     if (t_lo >= len_r) { s0 = -INFINITY; s1 = -INFINITY; }
     if (t_lo + 8 >= len_r) { s2 = -INFINITY; s3 = -INFINITY; }
     float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
@@ -356,7 +379,7 @@ __device__ __forceinline__ void load_q_frags(const __nv_bfloat16* qgroup, int G,
 // memory (reusing the tile area) and the CTAs' through cta_finish. Returns
 // true in the CTA that wrote the group's output; false in the others and when
 // any warp of the CTA failed (nothing is written then).
-template <int D, int NW, int STAGES>
+template <int D, int NW, int STAGES, bool KEEP_ML = false>
 __device__ __forceinline__ bool finish_bf16(const AttnK& a, uint8_t* tiles, bool ok,
                                             float (&o)[D / 16][4], float m0, float m1, float l0,
                                             float l1, int br, int g, int s_idx) {
@@ -398,7 +421,7 @@ __device__ __forceinline__ bool finish_bf16(const AttnK& a, uint8_t* tiles, bool
     }
   }
   __syncthreads();
-  return cta_finish<__nv_bfloat16, D, NW>(a, sm, br, g, s_idx);
+  return cta_finish<__nv_bfloat16, D, NW, KEEP_ML>(a, sm, br, g, s_idx);
 }
 
 }  // namespace resa

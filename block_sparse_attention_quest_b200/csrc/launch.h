@@ -73,6 +73,10 @@ struct AttnArgs {
   const int32_t* windows;
   double r;
   int n_min;
+  // weight-keeping decode (R = 1, every block): see AttnK
+  float* logits;
+  float* ml;
+  int64_t logit_stride;
 };
 cudaError_t launch_attend(const Shape& s, const AttnArgs& a, cudaStream_t st);
 
@@ -132,6 +136,29 @@ struct RectArgs {
 // dense rectification / prefill, then the split merge
 cudaError_t launch_rectify_tc(const RectArgs& r, cudaStream_t st);
 int attend_ctas_per_sm(const Shape& s);
+
+// attention weights and eviction (evict.cu) ---------------------------------------
+// weights[b][g][t] += sum over the group's heads of 2^(logit - m) / l; with
+// `fresh` the newest token's sum starts at this step
+cudaError_t launch_add_weights(const Shape& s, const float* logits, const float* ml,
+                               float* weights, int64_t len, const int32_t* lens, bool fresh,
+                               cudaStream_t st);
+struct EvictArgs {
+  const void* k;
+  const void* v;
+  const float* weights;   // [B][H][L_max]
+  int64_t len;
+  const int32_t* lens;    // optional per-row lengths [B]
+  int budget, recent;
+  int64_t L_out;          // capacity of the outputs
+  void* k_out;
+  void* v_out;
+  void* desc_out;         // or nullptr
+  float* weights_out;     // or nullptr
+  int32_t* kept;          // [B][H][budget]
+  Ctrl* ctrl;
+};
+cudaError_t launch_evict(const Shape& s, const EvictArgs& a, cudaStream_t st);
 
 // 4-bit cache (kv4.cuh) --------------------------------------------------------
 // rows of a cache to records and back; lens: optional per-row lengths [B]

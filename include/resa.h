@@ -290,6 +290,55 @@ RESA_API int resa_rectify_varlen(const resa_dims* dims, const void* q_f, const v
                                  int32_t f, float softmax_scale, void* out_f, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* ---- attention weights and eviction ----
+ * A budgeted cache beside the block-sparse one (no counterpart on the pages):
+ * decode steps add up how much attention every cached key receives, and
+ * resa_evict cuts the cache to the keys that received the most.
+ * lens is optional (NULL: every row has `len` tokens); with lens (DEVICE int32
+ * [batch]) `len` is the bound on its entries, as in the *_varlen calls.
+ *     weights   [batch][n_kv_heads][max_len]   float32, 16-byte aligned */
+
+/* Workspace bytes that suffice for resa_decode_dense_weights at any length up
+ * to `len` (a logit of every query head and token: 4 bytes each); 0 for
+ * invalid dims or len < 1. */
+RESA_API size_t resa_weights_workspace_bytes(const resa_dims* dims, int64_t len);
+
+/* resa_decode_dense (same arguments, same out and lse) that also adds each
+ * token's attention weight, summed over the group's query heads,
+ *     weights[b][g][t] += sum_{h in group g} exp(scale * q_h . k_t - lse_h),
+ * for t < len (lens[b]). With k_new the newest token's sum starts at this step
+ * (its slot is set, whatever it held); other slots keep adding up. Slots at or
+ * past the row's length are not touched. */
+RESA_API int resa_decode_dense_weights(const resa_dims* dims, const void* q, const void* k_new,
+                                       const void* v_new, void* k_cache, void* v_cache,
+                                       void* desc, float* weights, int64_t len,
+                                       const int32_t* lens, float softmax_scale, void* out,
+                                       float* lse, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* Every (row, KV head) cut to `budget` tokens: the newest n_recent
+ * (0 <= n_recent <= budget) and, of the others, the budget - n_recent of the
+ * largest weight (ties to the lower index; -0 equals +0, NaN ranks below every
+ * number), in their order. Rows of at most `budget` tokens are kept whole.
+ * With n' = min(row length, budget):
+ *  - k_out, v_out [batch][n_kv_heads][out_max_len][d] receive the kept rows in
+ *    slots [0, n'); out_max_len >= budget is a multiple of 16;
+ *  - desc_out [batch][n_kv_heads][out_max_len/16][2][d] (or NULL): their block
+ *    descriptors, as resa_build_desc(n') writes them;
+ *  - weights_out [batch][n_kv_heads][out_max_len] (or NULL): their weights;
+ *  - kept [batch][n_kv_heads][budget] int32: their old slots, ascending, then
+ *    -1 up to the budget.
+ * Slots and blocks past n' are not written. The outputs must not overlap the
+ * inputs or each other (RESA_ERR_INVALID_ARG). budget > out_max_len returns
+ * RESA_ERR_CAPACITY. The workspace only carries the error word:
+ * resa_workspace_bytes(dims, len, 0) suffices. Afterwards row b has
+ * min(lens[b], budget) tokens; each head's slots hold tokens of its own. */
+RESA_API int resa_evict(const resa_dims* dims, const void* k_cache, const void* v_cache,
+                        const float* weights, int64_t len, const int32_t* lens, int32_t budget,
+                        int32_t n_recent, int64_t out_max_len, void* k_out, void* v_out,
+                        void* desc_out, float* weights_out, int32_t* kept, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 /* ---- the cache in 4 bits ----
  * The pages run their INT4 series on the same method; the format below is this
  * library's. Sixteen tokens (one block) of one KV head form one record of
