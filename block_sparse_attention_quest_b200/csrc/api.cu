@@ -696,8 +696,7 @@ int resa_evict(const resa_dims* dims, const void* k_cache, const void* v_cache,
 // up to two pieces per CTA.
 static WsLayout kv4_layout(const Shape& s, int64_t len) {
   WsLayout w = ws_layout(s, len, 0);
-  const int64_t rows =
-      2 * static_cast<int64_t>(kv4_ctas(s, blocks_of(len), kKv4MaxCtas)) * s.G;
+  const int64_t rows = 2 * static_cast<int64_t>(kv4_most_ctas(s, blocks_of(len))) * s.G;
   size_t off = w.part_ml;
   off = align_up(off + static_cast<size_t>(rows) * 2 * sizeof(float));
   w.part_o = off;
@@ -776,7 +775,7 @@ static int run_kv4_attention(const Shape& s, const void* q, const void* kv4, int
   a.counters = reinterpret_cast<int*>(ws + w.counters);
   a.ctrl = reinterpret_cast<Ctrl*>(ws);
   a.out = out; a.lse = lse;
-  a.ctas = kv4_ctas(s, sel ? n_sel : blocks_of(len), num_sms);
+  a.ctas = kv4_ctas(s, sel ? n_sel : blocks_of(len), lens != nullptr, num_sms, &a.splits);
   return cuda_status(launch_kv4_attend(s, a, st));
 }
 

@@ -15,15 +15,19 @@
 // fp32 queries and fp32 p * vs enter as three bf16 parts each (24 bits), so an
 // fp32 call keeps fp32 accuracy.
 //
-// Work split: the blocks of every (row, KV head) in turn form one range, cut
-// into equal parts, one per CTA; a CTA walks the one or more (row, head)
-// pieces of its part. Rows of different lengths therefore load every CTA
-// alike. A piece that is not a whole (row, head) is left as a partial
-// (max, sum, accumulator) and the last CTA to arrive merges them in the order
-// of the range, so results do not depend on the arrival order.
+// Work split, one CTA per SM. With one length for every row each (row, KV
+// head) is cut into the same number of parts, one per CTA, wherever that
+// leaves few SMs idle. Otherwise the blocks of every (row, head) in turn form
+// one range, cut into equal parts; a CTA walks the pieces of its part, so rows
+// of different lengths load every CTA alike. (Each (row, head) also counts
+// kKv4PieceCost blocks for the fixed cost of a piece.) A piece that is not a
+// whole (row, head) is left as a partial (max, sum, accumulator) and the last
+// CTA to arrive merges them in the order of the range, so results do not
+// depend on the arrival order.
 //
-// Each warp streams whole records (one bulk copy per 16-token block, four in
-// flight) through its own ring in shared memory.
+// Each warp streams whole records (bulk copies, two blocks per stage) through
+// its own ring in shared memory; the copies of a CTA's next piece are under
+// way while the warps' results of the last one are merged.
 #include "kv4.cuh"
 
 #include "attend_core.cuh"
@@ -44,59 +48,81 @@ struct Kv4K {
   int64_t len;             // length, or the bound on the rows' lengths
   double r;                // with lens and sel: Eq. 5 of each row (r > 0)
   int n_min;
-  int B, H, G, Hq, Mmax, n_sel;
+  int B, H, G, Mmax, n_sel;
+  int splits;              // parts per (row, head) with a CTA each, or 0: parts of the range
   float scale_log2;
 };
 
-constexpr int kKv4Warps = 8;
-constexpr int kKv4Stages = 4;
-constexpr int kKv4MinBlocks = 8;   // blocks per CTA below which fewer CTAs are used
+// one CTA per SM; warps by the registers a warp needs (fp32 holds three parts
+// of q)
+template <typename T>
+constexpr int kKv4Warps = sizeof(T) == 2 ? 12 : 8;
+constexpr int kKv4Stages = 3;      // stages of two records per warp
+constexpr int kKv4MinBlocks = 16;  // blocks per CTA below which fewer CTAs are used
+// A piece's fixed cost, in blocks: its q, its first records' latency and the
+// merge of its warps, measured at 4.6 us where a block takes 72 ns (a batch of
+// 16 rows of 1K to 32K tokens; with 24 the CTAs of several short rows ended
+// last, 37 us after those of one long row).
+constexpr uint32_t kKv4PieceCost = 64;
 
-template <int D>
+template <typename T, int D>
 struct Kv4Cfg {
   static constexpr int kRec = kv4_record_bytes(D);
-  static constexpr int kRing = kKv4Warps * kKv4Stages * kRec;
-  static constexpr int kMerge = merge_floats(D, kKv4Warps) * 4;
-  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 128;
-  static_assert(kRing >= (8 * (kKv4MaxCtas + 2) + 8) * 4, "weights of the parts");
+  static constexpr int kRing = kKv4Warps<T> * kKv4Stages * 2 * kRec;
+  static constexpr int kMerge = merge_floats(D, kKv4Warps<T>) * 4;
+  static constexpr int kSmem = kRing + kMerge;
+  static_assert(kMerge >= (8 * (kKv4MaxCtas + 2) + 8) * 4, "weights of the parts");
 };
 
 // blocks of row b that its heads attend to
-__device__ __forceinline__ int kv4_row_blocks(const Kv4K& a, int b) {
+__device__ __forceinline__ uint32_t kv4_row_blocks(const Kv4K& a, int b) {
   const int64_t l = row_len(a.lens, a.len, b);
-  if (a.sel == nullptr) return static_cast<int>((l + kBlock - 1) / kBlock);
+  if (a.sel == nullptr) return static_cast<uint32_t>((l + kBlock - 1) / kBlock);
   return a.lens != nullptr ? num_selected_dev(l, a.r, a.n_min) : a.n_sel;
 }
 
-// One warp finds the row that holds position `x` of the range (or, with
-// x < 0, only the total).
-__device__ __forceinline__ void kv4_find(const Kv4K& a, long long x, long long& total, int& row,
-                                         long long& row_start) {
-  const int lane = threadIdx.x & 31;
-  if (a.lens == nullptr) {
-    const long long per = static_cast<long long>(a.H) * kv4_row_blocks(a, 0);
-    total = per * a.B;
-    row = x < 0 ? 0 : static_cast<int>(x / per);
-    row_start = row * per;
-    return;
+// The range of all (row, head) units, each kKv4PieceCost + its blocks long, and
+// its cut into equal parts (positions stay below 2^32: a cache has fewer than
+// 2^31 rows).
+struct Kv4Range {
+  uint32_t total, per, rem;
+  int ctas;
+  __device__ __forceinline__ void set(uint32_t n, uint32_t grid) {
+    total = n;
+    const uint32_t most = (n - 1) / (kKv4MinBlocks + kKv4PieceCost) + 1;
+    ctas = static_cast<int>(most < grid ? most : grid);
+    per = total / ctas;
+    rem = total - per * ctas;
   }
-  long long run = 0;
-  row = a.B;
+  // first position of CTA i's part
+  __device__ __forceinline__ uint32_t cut(uint32_t i) const { return i * per + min(i, rem); }
+  // the CTA whose part holds position x
+  __device__ __forceinline__ uint32_t owner(uint32_t x) const {
+    const uint32_t big = rem * (per + 1);
+    return x < big ? x / (per + 1) : rem + (x - big) / per;
+  }
+};
+
+// One warp finds the range's length and the row that holds position x.
+__device__ __forceinline__ void kv4_find(const Kv4K& a, uint32_t x, uint32_t& total, int& row,
+                                         uint32_t& row_start) {
+  const int lane = threadIdx.x & 31;
+  uint32_t run = 0;
+  row = 0;
   row_start = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
-    const long long mine = b < a.B ? static_cast<long long>(a.H) * kv4_row_blocks(a, b) : 0;
-    long long inc = mine;
-#pragma unroll
+    const uint32_t mine = b < a.B ? a.H * (kv4_row_blocks(a, b) + kKv4PieceCost) : 0u;
+    uint32_t inc = mine;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    const long long begin = run + inc - mine;
-    const bool here = x >= begin && x < begin + mine;
-    const unsigned who = __ballot_sync(0xffffffffu, here);
-    if (who) {
-      const int src = __ffs(who) - 1;
+    const uint32_t begin = run + inc - mine;
+    const unsigned who = __ballot_sync(0xffffffffu, b < a.B && x >= begin);
+    if (who) {                                    // the last row that begins at or before x
+      const int src = 31 - __clz(who);
       row = b0 + src;
       row_start = __shfl_sync(0xffffffffu, begin, src);
     }
@@ -105,45 +131,31 @@ __device__ __forceinline__ void kv4_find(const Kv4K& a, long long x, long long& 
   total = run;
 }
 
-// first position of CTA i's part
-__device__ __forceinline__ long long kv4_cut(long long total, int ctas, int i) {
-  return total * i / ctas;
-}
-// the CTA whose part holds position x
-__device__ __forceinline__ int kv4_owner(long long total, int ctas, long long x) {
-  int i = static_cast<int>((x * ctas) / total);
-  while (i + 1 < ctas && kv4_cut(total, ctas, i + 1) <= x) ++i;
-  while (kv4_cut(total, ctas, i) > x) --i;
-  return i;
-}
-
-// Merge of the partials of (row, head) u, whose blocks are [u0, u1) of the
-// range, by one CTA. The parts' (max, sum) pairs are turned into weights first,
-// then every thread sums pairs of output columns over the parts.
+// Merge of the partials that `parts` consecutive CTAs from `first` on left of one
+// (row, head), by one CTA. `late`: the first of them began before this (row,
+// head), so it is that CTA's last piece. The (max, sum) pairs are turned into
+// weights first, then every thread sums pairs of output columns over the parts.
 template <typename T, int D>
-__device__ __forceinline__ void kv4_merge(const Kv4K& a, float* sm, long long total, int ctas,
-                                          long long u0, long long u1, int64_t head0) {
-  constexpr int NT = kKv4Warps * 32;
-  const int first = kv4_owner(total, ctas, u0), last = kv4_owner(total, ctas, u1 - 1);
-  const int n = last - first + 1;
+__device__ __forceinline__ void kv4_merge(const Kv4K& a, float* sm, int first, int parts,
+                                          bool late, int64_t head0) {
+  constexpr int NW = kKv4Warps<T>, NT = NW * 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto slot = [&](int s) -> int64_t {
-    // a part that began before the unit's first block holds it as its last piece
-    return 2 * static_cast<int64_t>(first + s) +
-           (s == 0 && kv4_cut(total, ctas, first) < u0 ? 1 : 0);
-  };
-  float* w_s = sm;                      // [n][8] weights
+  auto slot = [&](int s) -> int { return 2 * (first + s) + (s == 0 && late ? 1 : 0); };
+  float* w_s = sm;                      // [parts][8] weights
   float* l_h = sm + 8 * (kKv4MaxCtas + 2);
-  for (int h = warp; h < a.G; h += kKv4Warps) {
-    float m = -INFINITY;
-    for (int s = lane; s < n; s += 32) m = fmaxf(m, __ldcg(a.part_ml + (slot(s) * a.G + h) * 2));
+  for (int h = warp; h < a.G; h += NW) {
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + h;
+    // (the usual number of parts is at most 32: one load per lane)
+    const float2 mine = lane < parts ? __ldcg(ml + slot(lane) * a.G) : make_float2(-INFINITY, 0.f);
+    float m = mine.x;
+    for (int s = lane + 32; s < parts; s += 32) m = fmaxf(m, __ldcg(ml + slot(s) * a.G).x);
     m = warp_max_xor(m, 16, 1);
     float l = 0.f;
-    for (int s = lane; s < n; s += 32) {
-      const float ms = __ldcg(a.part_ml + (slot(s) * a.G + h) * 2);
-      const float w = ms == -INFINITY ? 0.f : exp2f(ms - m);
+    for (int s = lane; s < parts; s += 32) {
+      const float2 p = s == lane ? mine : __ldcg(ml + slot(s) * a.G);
+      const float w = p.x == -INFINITY ? 0.f : exp2f(p.x - m);
       w_s[s * 8 + h] = w;
-      l = fmaf(w, __ldcg(a.part_ml + (slot(s) * a.G + h) * 2 + 1), l);
+      l = fmaf(w, p.y, l);
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -152,28 +164,34 @@ __device__ __forceinline__ void kv4_merge(const Kv4K& a, float* sm, long long to
       if (a.lse != nullptr) a.lse[head0 + h] = (m + log2f(l)) * 0.69314718055994531f;
     }
   }
-  __syncthreads();
   T* out = static_cast<T*>(a.out);
-  for (int i = threadIdx.x; i < a.G * (D / 2); i += NT) {
+  for (int i0 = 0; i0 < a.G * (D / 2); i0 += NT) {
+    const int i = i0 + threadIdx.x;
+    const bool in = i < a.G * (D / 2);
     const int h = i / (D / 2), c = (i % (D / 2)) * 2;
+    const float* po = a.part_o + h * D + c;
     float o0 = 0.f, o1 = 0.f;
-    for (int s0 = 0; s0 < n; s0 += 16) {
-      float2 x[16];
+    for (int s0 = 0; s0 < parts; s0 += 24) {
+      float2 x[24];
 #pragma unroll
-      for (int u = 0; u < 16; ++u)
-        if (s0 + u < n)
-          x[u] = __ldcg(reinterpret_cast<const float2*>(a.part_o + (slot(s0 + u) * a.G + h) * D + c));
+      for (int u = 0; u < 24; ++u)
+        if (in && s0 + u < parts)
+          x[u] = __ldcg(reinterpret_cast<const float2*>(
+              po + static_cast<int64_t>(slot(s0 + u)) * a.G * D));
+      if (i0 == 0 && s0 == 0) __syncthreads();     // the weights, behind the first loads
 #pragma unroll
-      for (int u = 0; u < 16; ++u)
-        if (s0 + u < n) {
+      for (int u = 0; u < 24; ++u)
+        if (in && s0 + u < parts) {
           const float w = w_s[(s0 + u) * 8 + h];
           o0 = fmaf(w, x[u].x, o0);
           o1 = fmaf(w, x[u].y, o1);
         }
     }
-    const float inv = 1.f / l_h[h];
-    out[(head0 + h) * D + c] = Dt<T>::from_f(o0 * inv);
-    out[(head0 + h) * D + c + 1] = Dt<T>::from_f(o1 * inv);
+    if (in) {
+      const float inv = 1.f / l_h[h];
+      out[(head0 + h) * D + c] = Dt<T>::from_f(o0 * inv);
+      out[(head0 + h) * D + c + 1] = Dt<T>::from_f(o1 * inv);
+    }
   }
 }
 
@@ -188,21 +206,65 @@ __device__ __forceinline__ void bf16_parts(float x, float (&p)[PARTS]) {
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kKv4Warps * 32, sizeof(T) == 2 ? 2 : 1)
+// What the end of a piece needs, kept in shared memory while its blocks stream.
+struct Kv4Done {
+  int64_t bh;
+  int slot;                // partial slot, or -1 when the piece is the whole unit
+  int first, parts, late;  // the unit's partials: see kv4_merge
+};
+
+// mma_bf16_16816 with rows 8 .. 15 of the sum left out.
+__device__ __forceinline__ void mma_row0(float& d0, float& d1, const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  [[maybe_unused]] float x2, x3;
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%10,%10};"
+      : "+f"(d0), "+f"(d1), "=f"(x2), "=f"(x3)
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// 2^x; results below 2^-126 are 0 (weights that small change no sum here)
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A warp takes two blocks at a time (one stage of its ring): the two
+// independent chains of products and exponentials hide each other's latency,
+// and the barrier, the check of the running maximum and the loop's own
+// instructions are shared. Weights p carry a factor 2^64 throughout (in the
+// exponent, for nothing), which is what keeps products with subnormal codes
+// normal numbers.
+//
+// Rounding p * scale to bf16 costs 2^-9 of each term p * scale * code, and the
+// codes' common part (their mean is near 8 of 15) would make that error three
+// times the bf16 cache's. So the products are taken about code 8: the sum of
+// the rounded p * scale (one product with a constant matrix of ones per group)
+// times 8 is subtracted at the end, exactly, and zero + 8 * scale takes the
+// place of the zero. (Measured at a 128K context: error against 64 bits 4.8e-3
+// without, 2.4e-3 with it, 1.7e-3 being the output's own rounding.) An fp32
+// call subtracts 8 * p * scale inside the product, so that its sums stay small.
+template <typename T, int D, bool SEL>
+__global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     kv4_attend_kernel(Kv4K a) {
-  using C = Kv4Cfg<D>;
+  using C = Kv4Cfg<T, D>;
   constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;    // bf16 parts of q and of p * scale
   constexpr int NG = D / kKv4Group;
-  constexpr int NW = kKv4Warps, ST = kKv4Stages, REC = C::kRec;
+  constexpr int NW = kKv4Warps<T>, ST = kKv4Stages, REC = C::kRec;
   constexpr float kUp = 18446744073709551616.f;                 // 2^64
   constexpr float kDown = 5.9029581035870565e+20f;              // 2^69
-  extern __shared__ uint8_t smem_raw[];
+  constexpr uint32_t kOnes = 0x00010001u;                       // code 1 in both halves
+  constexpr float kMid = 8.f;                                   // code the products are taken about
+  constexpr float kMidK = PARTS == 1 ? 0.f : 8.f;
+  constexpr uint32_t kNeg8 = 0x80088008u, kNeg128 = 0x80808080u;   // -8 and, where codes count 16-fold, -8 * 16
+  extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(8) uint64_t bars[NW][ST];
-  __shared__ long long s_total, s_row_start;
+  __shared__ uint32_t s_total, s_row_start;
   __shared__ int s_row, s_last;
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
-                                             ~static_cast<uintptr_t>(127));
+  __shared__ float s_mx[8], s_l[8];
+  __shared__ Kv4Done s_done[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, cq = lane & 3;
   if (lane == 0) {
@@ -210,102 +272,181 @@ __global__ void __launch_bounds__(kKv4Warps * 32, sizeof(T) == 2 ? 2 : 1)
     for (int st = 0; st < ST; ++st) mbar_init(&bars[warp][st], 1);
     fence_mbar_init();
   }
+  __syncwarp();
   // everything read below may come from the kernel before this one
   grid_dependency_wait();
-  if (warp == 0) {
-    long long total, start;
-    int row;
-    kv4_find(a, -1, total, row, start);
-    const long long most = (total + kKv4MinBlocks - 1) / kKv4MinBlocks;
-    const int n = static_cast<int>(most < gridDim.x ? most : gridDim.x);
-    if (static_cast<int>(blockIdx.x) < n)
-      kv4_find(a, kv4_cut(total, n, blockIdx.x), total, row, start);
-    if (lane == 0) { s_total = total; s_row = row; s_row_start = start; }
-  }
-  if (a.lens != nullptr && blockIdx.x == 0)
-    for (int b = threadIdx.x; b < a.B; b += NW * 32)
-      if (row_len_bad(a.lens, a.len, b)) raise_error(a.ctrl, kErrBadIndex);
-  __syncthreads();
-  const long long total = s_total;
-  const long long most = (total + kKv4MinBlocks - 1) / kKv4MinBlocks;
-  const int ctas = static_cast<int>(most < gridDim.x ? most : gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const long long part0 = kv4_cut(total, ctas, blockIdx.x);
-  const long long part1 = kv4_cut(total, ctas, blockIdx.x + 1);
-  int row = s_row;
-  long long row_start = s_row_start;
-  uint8_t* my_ring = ring + warp * ST * REC;
-  uint32_t issued = 0, used = 0;                  // records of this warp's ring, over all pieces
-  bool ok = true;
-
-  for (long long x = part0; x < part1;) {
-    // ---- the piece [x, x_end) of (row, head) g
-    int m_row = kv4_row_blocks(a, row);
-    while (x >= row_start + static_cast<long long>(m_row) * a.H) {
-      row_start += static_cast<long long>(m_row) * a.H;
-      m_row = kv4_row_blocks(a, ++row);
-    }
-    const int g = static_cast<int>((x - row_start) / m_row);
-    const long long u0 = row_start + static_cast<long long>(g) * m_row, u1 = u0 + m_row;
-    const long long x_end = u1 < part1 ? u1 : part1;
-    const int i0 = static_cast<int>(x - u0), i1 = static_cast<int>(x_end - u0);
-    const int64_t bh = static_cast<int64_t>(row) * a.H + g;
-    const int64_t len_r = row_len(a.lens, a.len, row);
-    const int blocks_r = static_cast<int>((len_r + kBlock - 1) / kBlock);
-    const int32_t* selp = a.sel ? a.sel + bh * a.n_sel : nullptr;
-    const uint8_t* base = a.kv4 + bh * a.Mmax * REC;
-    const int64_t head0 = static_cast<int64_t>(row) * a.Hq + g * a.G;
-    const int span = i1 - i0;
-    const int count = span > warp ? (span - warp + NW - 1) / NW : 0;
-    // this warp's k-th block is number i0 + warp + k NW of the list; lane u
-    // holds the ids of blocks 32 w + u of its own sequence
-    int ids = -1;
-    auto load_ids = [&](int k0) {
-      const int k = k0 + lane;
-      ids = -1;
-      if (k < count) {
-        const int i = i0 + warp + k * NW;
-        const int j = selp ? __ldg(selp + i) : i;
-        ids = j >= 0 && j < blocks_r ? j : -1;
+  // ---- this CTA's part: one part of one unit (a.splits per unit), or a
+  // stretch of the range
+  Kv4Range range;
+  uint32_t x = 0, part1 = 0, row_start = 0, m_row;
+  int row;
+  if (a.splits > 0) {
+    m_row = kv4_row_blocks(a, 0);
+    row = static_cast<int>(blockIdx.x) / (a.splits * a.H);
+  } else {
+    if (a.lens == nullptr) {
+      m_row = kv4_row_blocks(a, 0);
+      const uint32_t per_row = a.H * (m_row + kKv4PieceCost);
+      range.set(per_row * a.B, gridDim.x);
+      if (static_cast<int>(blockIdx.x) >= range.ctas) return;
+      row = static_cast<int>(range.cut(blockIdx.x) / per_row);
+      row_start = row * per_row;
+    } else {
+      if (warp == 0) {
+        uint32_t n, start;
+        int r;
+        kv4_find(a, 0u, n, r, start);
+        range.set(n, gridDim.x);
+        kv4_find(a, range.cut(blockIdx.x), n, r, start);
+        if (lane == 0) { s_total = n; s_row = r; s_row_start = start; }
+      } else if (blockIdx.x == 0) {
+        for (int b = threadIdx.x - 32; b < a.B; b += (NW - 1) * 32)
+          if (row_len_bad(a.lens, a.len, b)) raise_error(a.ctrl, kErrBadIndex);
       }
-    };
-    // the blocks copied run ST ahead of those in use: ids holds the 32 ids
-    // around the former, ids_now those around the latter
-    load_ids(0);
-    int ids_now = ids;
-    auto issue = [&](int k) {                     // whole warp
-      const int j = __shfl_sync(0xffffffffu, ids, k & 31);
+      __syncthreads();
+      range.set(s_total, gridDim.x);
+      if (static_cast<int>(blockIdx.x) >= range.ctas) return;
+      row = s_row;
+      row_start = s_row_start;
+      m_row = kv4_row_blocks(a, row);
+    }
+    x = range.cut(blockIdx.x);
+    part1 = range.cut(blockIdx.x + 1);
+  }
+  const uint32_t part0 = x;
+  uint8_t* my_ring = ring + warp * ST * 2 * REC;
+  uint32_t used = 0;                              // stages of this warp's ring, over all pieces
+
+  // ---- the piece at hand: entries [i0, i1) of unit bh's blocks (or list)
+  int i0, i1, count, tail, part_block, blocks_r, ids = -1, ids_now = -1;
+  int64_t bh;
+  const uint8_t* base;
+  constexpr int QW = sizeof(T);                   // 16-byte words of 16 channels
+  uint4 qraw[NG][QW];                             // head gq's channels 64 g + 16 cq .. + 15
+#pragma unroll
+  for (int i = 0; i < NG; ++i)
+#pragma unroll
+    for (int j = 0; j < QW; ++j) qraw[i][j] = make_uint4(0u, 0u, 0u, 0u);
+  // With a list, lane u of `ids` holds entry u % 2 of this warp's pair
+  // 16 w + u / 2 around the pair copied next, `ids_now` those around the pair
+  // in use; pair k is entries i0 + 2 (warp + k NW) and the next.
+  auto load_ids = [&](int k0) {
+    const int i = i0 + 2 * (warp + (k0 + (lane >> 1)) * NW) + (lane & 1);
+    ids = -1;
+    if (i < i1) {
+      const int j = __ldg(a.sel + bh * a.n_sel + i);
+      if (j >= 0 && j < blocks_r) ids = j;
+      else raise_error(a.ctrl, kErrBadIndex);      // the block is skipped
+    }
+  };
+  auto issue = [&](int k, int st) {               // pair k into stage st; whole warp
+    uint64_t* bar = &bars[warp][st];
+    uint8_t* dst = my_ring + st * 2 * REC;
+    if constexpr (SEL) {
+      if ((k & 15) == 0) load_ids(k);
+      const int ja = __shfl_sync(0xffffffffu, ids, (2 * k) & 31);
+      const int jb = __shfl_sync(0xffffffffu, ids, (2 * k + 1) & 31);
       if (lane == 0) {
         fence_proxy_async_smem();                 // the stage's last reads precede the copy
-        uint64_t* bar = &bars[warp][issued % ST];
-        mbar_arrive_expect_tx(bar, REC);
-        // (a bad id still fills the stage, with block 0)
-        bulk_load(my_ring + (issued % ST) * REC, base + static_cast<int64_t>(j < 0 ? 0 : j) * REC,
-                  REC, bar);
+        mbar_arrive_expect_tx(bar, ((ja >= 0) + (jb >= 0)) * REC);
+        if (ja >= 0) bulk_load(dst, base + static_cast<int64_t>(ja) * REC, REC, bar);
+        if (jb >= 0) bulk_load(dst + REC, base + static_cast<int64_t>(jb) * REC, REC, bar);
       }
-      ++issued;
-    };
-    for (int k = 0; k < count && k < ST; ++k) issue(k);
+    } else {
+      if (lane == 0) {
+        const int i = i0 + 2 * (warp + k * NW);
+        const uint32_t bytes = i + 1 < i1 ? 2 * REC : REC;
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(bar, bytes);
+        bulk_load(dst, base + static_cast<int64_t>(i) * REC, bytes, bar);
+      }
+    }
+  };
+  // Moves to the next piece (from x on), starts its copies and notes in
+  // `done` what its end needs; false when there is none.
+  auto next_piece = [&](Kv4Done& done) -> bool {
+    int g;
+    if (a.splits > 0) {
+      if (x != 0) return false;
+      x = 1;
+      const int part = static_cast<int>(blockIdx.x) % a.splits;
+      g = static_cast<int>(blockIdx.x) / a.splits % a.H;
+      const int per = m_row / a.splits, rem = m_row % a.splits;
+      i0 = part * per + min(part, rem);
+      i1 = i0 + per + (part < rem);
+      bh = static_cast<int64_t>(row) * a.H + g;
+      if (threadIdx.x == 0) {
+        done.bh = bh;
+        done.slot = a.splits == 1 ? -1 : 2 * static_cast<int>(blockIdx.x);
+        done.first = static_cast<int>(blockIdx.x) - part; done.parts = a.splits; done.late = 0;
+      }
+    } else {
+      uint32_t u0, u1, from;
+      do {
+        if (x >= part1) return false;
+        while (x - row_start >= a.H * (m_row + kKv4PieceCost)) {
+          row_start += a.H * (m_row + kKv4PieceCost);
+          m_row = kv4_row_blocks(a, ++row);
+        }
+        g = static_cast<int>((x - row_start) / (m_row + kKv4PieceCost));
+        u0 = row_start + g * (m_row + kKv4PieceCost);
+        u1 = u0 + kKv4PieceCost + m_row;
+        from = x;
+        x = min(u1, part1);
+        i0 = static_cast<int>(max(from, u0 + kKv4PieceCost) - (u0 + kKv4PieceCost));
+        i1 = static_cast<int>(max(x, u0 + kKv4PieceCost) - (u0 + kKv4PieceCost));
+      } while (i0 >= i1);                         // (a unit's cost without its blocks)
+      bh = static_cast<int64_t>(row) * a.H + g;
+      if (threadIdx.x == 0) {
+        done.bh = bh;
+        // slot 0: a part that begins in its first piece's unit; slot 1: its last piece
+        done.slot = i0 == 0 && i1 == static_cast<int>(m_row)
+                        ? -1 : 2 * static_cast<int>(blockIdx.x) + (from == part0 ? 0 : 1);
+        if (done.slot >= 0) {
+          done.first = static_cast<int>(range.owner(u0 + kKv4PieceCost));
+          done.parts = static_cast<int>(range.owner(u1 - 1)) - done.first + 1;
+          done.late = range.cut(done.first) < u0;
+        }
+      }
+    }
+    const int64_t len_r = row_len(a.lens, a.len, row);
+    blocks_r = static_cast<int>((len_r + kBlock - 1) / kBlock);
+    // tokens of the row's last block, and its number where it is not full
+    tail = static_cast<int>(len_r & (kBlock - 1));
+    part_block = tail ? blocks_r - 1 : -2;
+    base = a.kv4 + bh * a.Mmax * REC;
+    // (ahead of the copies, which it would queue behind)
+    if (gq < a.G) {
+      const T* qg = static_cast<const T*>(a.q) + (bh * a.G + gq) * D + cq * 16;
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int j = 0; j < QW; ++j)
+          qraw[i][j] = ldg16(reinterpret_cast<const uint4*>(qg + i * 64) + j);
+    }
+    const int pairs = (i1 - i0 + 1) / 2;
+    count = pairs > warp ? (pairs - warp + NW - 1) / NW : 0;
+    for (int k = 0; k < count && k < ST; ++k) issue(k, (used + k) % ST);
+    return true;
+  };
 
+  bool more = next_piece(s_done[0]);
+#pragma unroll 1
+  for (int piece = 0; more; ++piece) {
+    bool ok = true;
     // ---- q fragments and the group sums of q
     uint32_t qb[PARTS][NG * 4][2];
     float qs0[NG], qs1[NG];
     {
-      const T* qg = static_cast<const T*>(a.q) + head0 * D;
 #pragma unroll
       for (int g2 = 0; g2 < NG; ++g2) {
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float f[8];
-          if (gq < a.G) {
-            const T* p = qg + gq * D + g2 * 64 + cq * 16 + j * 8;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = Dt<T>::to_f(p[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = 0.f;
-          }
+          for (int i = 0; i < QW / 2; ++i)
+            Chunk<T>::unpack(qraw[g2][j * (QW / 2) + i], f + i * Chunk<T>::N);
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum += f[i];
           float part[8][PARTS];
@@ -325,91 +466,127 @@ __global__ void __launch_bounds__(kKv4Warps * 32, sizeof(T) == 2 ? 2 : 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         // heads 2 cq and 2 cq + 1 of the result layout, in the sums' scale
-        qs0[g2] = __shfl_sync(0xffffffffu, sum, 8 * cq) / kDown;
-        qs1[g2] = __shfl_sync(0xffffffffu, sum, 8 * cq + 4) / kDown;
+        qs0[g2] = __shfl_sync(0xffffffffu, sum, 8 * cq) * (1.f / kDown);
+        qs1[g2] = __shfl_sync(0xffffffffu, sum, 8 * cq + 4) * (1.f / kDown);
       }
     }
     const float to_log2 = a.scale_log2 * kDown;
 
-    float o[NG * 4][4], zo0[NG], zo1[NG];
+    float o[NG * 4][4], ones[NG][2], zo0[NG], zo1[NG];
 #pragma unroll
     for (int i = 0; i < NG * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 #pragma unroll
-    for (int i = 0; i < NG; ++i) { zo0[i] = 0.f; zo1[i] = 0.f; }
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    for (int i = 0; i < NG; ++i) {
+      ones[i][0] = 0.f; ones[i][1] = 0.f;
+      zo0[i] = 0.f; zo1[i] = 0.f;
+    }
+    // n = 64 - m with m the reference (log2 units) of the weights 2^(s + n)
+    float n0 = INFINITY, n1 = INFINITY, l0 = 0.f, l1 = 0.f;
 
     for (int k = 0; k < count; ++k) {
-      if ((k & 31) == 0) ids_now = ids;           // (loaded when block k was issued)
       const int st = used % ST;
-      const bool arrived = mbar_wait_bounded(&bars[warp][st], (used / ST) & 1, a.ctrl);
-      if (!__all_sync(0xffffffffu, arrived)) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, mbar_try_wait(&bars[warp][st], (used / ST) & 1))) {
+        const bool arrived = mbar_wait_bounded(&bars[warp][st], (used / ST) & 1, a.ctrl);
+        if (!__all_sync(0xffffffffu, arrived)) { ok = false; break; }
+      }
       ++used;
-      const int j = __shfl_sync(0xffffffffu, ids_now, k & 31);
-      const uint8_t* rec = my_ring + st * REC;
-      uint4 kw[NG], vw[NG];
-      uint2 meta[2][NG];                          // [token half][group]: {ks kz}, {vs vz}
-#pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        kw[i] = *reinterpret_cast<const uint4*>(rec + i * 512 + lane * 16);
-        vw[i] = *reinterpret_cast<const uint4*>(rec + kv4_code_bytes(D) + i * 512 + lane * 16);
+      const uint8_t* rec = my_ring + st * 2 * REC + lane * 16;
+      const uint8_t* met = my_ring + st * 2 * REC + 2 * kv4_code_bytes(D) + gq * 16 * NG;
+      // tokens of the two blocks that count (16 and 16 but for a row's last
+      // block, an odd list's end, an id out of range)
+      int ja, jb, va = kBlock, vb = kBlock;
+      if constexpr (SEL) {
+        if ((k & 15) == 0) ids_now = ids;       // (pairs k .. k + 15, loaded at pair k's issue)
+        ja = __shfl_sync(0xffffffffu, ids_now, (2 * k) & 31);
+        jb = __shfl_sync(0xffffffffu, ids_now, (2 * k + 1) & 31);
+      } else {
+        ja = i0 + 2 * (warp + k * NW);
+        jb = ja + 1 < i1 ? ja + 1 : -1;
       }
+      if (ja == part_block) va = tail;
+      if (jb == part_block) vb = tail;
+      if (ja < 0) va = 0;
+      if (jb < 0) vb = 0;
+      const bool whole = va + vb == 2 * kBlock;   // warp-uniform
+
+      // ---- logits of tokens gq, gq + 8 of both blocks, heads 2 cq, 2 cq + 1
+      float s[2][4];
+      uint32_t vm[2][2][NG];                      // [block][token half][group]: {vs vz}
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int u = 0; u < 2; ++u) {
+        s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
+        uint2 meta[2][NG];
 #pragma unroll
-        for (int i = 0; i < NG; ++i)
-          meta[h][i] = *reinterpret_cast<const uint2*>(rec + 2 * kv4_code_bytes(D) +
-                                                       ((gq * 2 + h) * NG + i) * 8);
-      __syncwarp();                               // every lane has read the record
-      if (k + ST < count) {
-        if (((k + ST) & 31) == 0) load_ids(k + ST);
-        issue(k + ST);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < NG; ++i)
+            meta[h][i] = *reinterpret_cast<const uint2*>(met + u * REC + (h * NG + i) * 8);
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          const uint4 kw = *reinterpret_cast<const uint4*>(rec + u * REC + i * 512);
+          // (fp32 takes keys about code kMidK too: smaller sums, smaller errors)
+          float acc[4] = {-kMidK * qs0[i], -kMidK * qs1[i], -kMidK * qs0[i], -kMidK * qs1[i]};
+          const uint32_t wa[2] = {kw.x, kw.y}, wb[2] = {kw.z, kw.w};
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t x0 = wa[w] >> (8 * e), x1 = wb[w] >> (8 * e);
+              const uint32_t af[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u,
+                                      x1 & 0x00f000f0u};
+#pragma unroll
+              for (int p = 0; p < PARTS; ++p)
+                mma_bf16_16816(acc, af, qb[p][i * 4 + 2 * w + e][0], qb[p][i * 4 + 2 * w + e][1]);
+            }
+          }
+          const float ka = bf16_lo(meta[0][i].x), kb = bf16_lo(meta[1][i].x);
+          const float za = fmaf(kMidK, ka, bf16_hi(meta[0][i].x));
+          const float zb = fmaf(kMidK, kb, bf16_hi(meta[1][i].x));
+          s[u][0] = fmaf(ka, acc[0], fmaf(za, qs0[i], s[u][0]));
+          s[u][1] = fmaf(ka, acc[1], fmaf(za, qs1[i], s[u][1]));
+          s[u][2] = fmaf(kb, acc[2], fmaf(zb, qs0[i], s[u][2]));
+          s[u][3] = fmaf(kb, acc[3], fmaf(zb, qs1[i], s[u][3]));
+          vm[u][0][i] = meta[0][i].y;
+          vm[u][1][i] = meta[1][i].y;
+        }
       }
-      if (j < 0) {                                // skip the block, report it
-        if (lane == 0) raise_error(a.ctrl, kErrBadIndex);
-        continue;
-      }
-      // ---- logits of tokens gq, gq + 8 and heads 2 cq, 2 cq + 1
-      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+      // tokens that do not count: weight 0, and their scales (which may be
+      // anything) with it; their codes are finite whatever the bits
+      if (!whole) {
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t wa[2] = {kw[i].x, kw[i].y}, wb[2] = {kw[i].z, kw[i].w};
+        for (int u = 0; u < 2; ++u) {
+          const int valid = u == 0 ? va : vb;
+          if (gq >= valid) { s[u][0] = -INFINITY; s[u][1] = -INFINITY; }
+          if (gq + 8 >= valid) { s[u][2] = -INFINITY; s[u][3] = -INFINITY; }
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const uint32_t x0 = wa[w] >> (8 * s), x1 = wb[w] >> (8 * s);
-            const uint32_t af[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u,
-                                    x1 & 0x00f000f0u};
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p)
-              mma_bf16_16816(acc, af, qb[p][i * 4 + 2 * w + s][0], qb[p][i * 4 + 2 * w + s][1]);
+          for (int i = 0; i < NG; ++i) {
+            if (gq >= valid) vm[u][0][i] = 0u;
+            if (gq + 8 >= valid) vm[u][1][i] = 0u;
           }
         }
-        const float ka = bf16_lo(meta[0][i].x), za = bf16_hi(meta[0][i].x);
-        const float kb = bf16_lo(meta[1][i].x), zb = bf16_hi(meta[1][i].x);
-        s0 = fmaf(ka, acc[0], fmaf(za, qs0[i], s0));
-        s1 = fmaf(ka, acc[1], fmaf(za, qs1[i], s1));
-        s2 = fmaf(kb, acc[2], fmaf(zb, qs0[i], s2));
-        s3 = fmaf(kb, acc[3], fmaf(zb, qs1[i], s3));
+        if (va + vb == 0) {                       // (both ids out of range)
+          __syncwarp();
+          if (k + ST < count) issue(k + ST, st);
+          continue;
+        }
       }
-      s0 *= to_log2; s1 *= to_log2; s2 *= to_log2; s3 *= to_log2;
-      // tokens past the end: weight 0, and neither their codes (any four
-      // bits are finite) nor their scales (masked below) reach an output
-      const int64_t t_lo = static_cast<int64_t>(j) * kBlock + gq;
-      const bool va = t_lo < len_r, vb = t_lo + 8 < len_r;
-      if (!va) { s0 = -INFINITY; s1 = -INFINITY; }
-      if (!vb) { s2 = -INFINITY; s3 = -INFINITY; }
-      // the reference moves only when some token exceeds it by 2^8: p, the
-      // sums and the outputs stay far inside fp32, and most blocks rescale
-      // nothing
-      const float b0 = fmaxf(s0, s2), b1 = fmaxf(s1, s3);
-      if (__any_sync(0xffffffffu, b0 > m0 + 8.f || b1 > m1 + 8.f)) {
-        const float n0 = fmaxf(m0, warp_max_xor(b0, 16, 4));
-        const float n1 = fmaxf(m1, warp_max_xor(b1, 16, 4));
-        const float al0 = m0 == -INFINITY ? 0.f : exp2f(m0 - n0);
-        const float al1 = m1 == -INFINITY ? 0.f : exp2f(m1 - n1);
-        m0 = n0; m1 = n1;
+      // The reference moves only when some weight would exceed it by 2^8: the
+      // sums stay far inside fp32, and most pairs rescale nothing.
+      // (The product is rounded before n is added: with one rounding of both,
+      // logits beyond 2^24 would leave a difference of any size.)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[u][e] = __fmul_rn(s[u][e], to_log2);
+      const float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+      const float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+      // (n = infinity before the first pair, where the sum is infinite or NaN)
+      if (__any_sync(0xffffffffu, !(x0 + n0 <= 72.f && x1 + n1 <= 72.f))) {
+        const float r0 = fminf(n0, 64.f - warp_max_xor(x0, 16, 4));
+        const float r1 = fminf(n1, 64.f - warp_max_xor(x1, 16, 4));
+        const float al0 = n0 == INFINITY ? 0.f : ex2_ftz(r0 - n0);
+        const float al1 = n1 == INFINITY ? 0.f : ex2_ftz(r1 - n1);
+        n0 = r0; n1 = r1;
         l0 *= al0; l1 *= al1;
 #pragma unroll
         for (int i = 0; i < NG * 4; ++i) {
@@ -417,23 +594,26 @@ __global__ void __launch_bounds__(kKv4Warps * 32, sizeof(T) == 2 ? 2 : 1)
           o[i][1] *= al1; o[i][3] *= al1;
         }
 #pragma unroll
-        for (int i = 0; i < NG; ++i) { zo0[i] *= al0; zo1[i] *= al1; }
+        for (int i = 0; i < NG; ++i) {
+          zo0[i] *= al0; zo1[i] *= al1;
+          ones[i][0] *= al0; ones[i][1] *= al1;
+        }
       }
-      const float p0 = exp2f(s0 - m0), p1 = exp2f(s1 - m1);
-      const float p2 = exp2f(s2 - m0), p3 = exp2f(s3 - m1);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      // ---- values
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        const float sa = va ? bf16_lo(meta[0][i].y) * kUp : 0.f;
-        const float sb = vb ? bf16_lo(meta[1][i].y) * kUp : 0.f;
-        const float za = va ? bf16_hi(meta[0][i].y) : 0.f;
-        const float zb = vb ? bf16_hi(meta[1][i].y) : 0.f;
-        zo0[i] = fmaf(p0, za, fmaf(p2, zb, zo0[i]));
-        zo1[i] = fmaf(p1, za, fmaf(p3, zb, zo1[i]));
-        uint32_t pb[PARTS][2];
-        {
+      for (int u = 0; u < 2; ++u) {
+        const float p0 = ex2_ftz(s[u][0] + n0), p1 = ex2_ftz(s[u][1] + n1);
+        const float p2 = ex2_ftz(s[u][2] + n0), p3 = ex2_ftz(s[u][3] + n1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        // ---- values
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          const float sa = bf16_lo(vm[u][0][i]), sb = bf16_lo(vm[u][1][i]);
+          const float za = fmaf(kMid, sa, bf16_hi(vm[u][0][i]));
+          const float zb = fmaf(kMid, sb, bf16_hi(vm[u][1][i]));
+          zo0[i] = fmaf(p0, za, fmaf(p2, zb, zo0[i]));
+          zo1[i] = fmaf(p1, za, fmaf(p3, zb, zo1[i]));
+          uint32_t pb[PARTS][2];
           float e0[PARTS], e1[PARTS], e2[PARTS], e3[PARTS];
           if constexpr (PARTS == 1) {
             e0[0] = p0 * sa; e1[0] = p1 * sa; e2[0] = p2 * sb; e3[0] = p3 * sb;
@@ -443,34 +623,45 @@ __global__ void __launch_bounds__(kKv4Warps * 32, sizeof(T) == 2 ? 2 : 1)
             bf16_parts<PARTS>(p2 * sb, e2);
             bf16_parts<PARTS>(p3 * sb, e3);
           }
+          const uint32_t one[4] = {kOnes, kOnes, kOnes, kOnes};
 #pragma unroll
           for (int p = 0; p < PARTS; ++p) {
             pb[p][0] = movmatrix_trans(pack_bf16x2(e0[p], e1[p]));
             pb[p][1] = movmatrix_trans(pack_bf16x2(e2[p], e3[p]));
+            if constexpr (PARTS == 1) mma_row0(ones[i][0], ones[i][1], one, pb[p][0], pb[p][1]);
+          }
+          const uint4 vw = *reinterpret_cast<const uint4*>(rec + u * REC + kv4_code_bytes(D) + i * 512);
+          const uint32_t w4[4] = {vw.x, vw.y, vw.z, vw.w};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t x0 = w4[m], x1 = w4[m] >> 8;
+            const uint32_t af[4] = {x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu,
+                                    x1 & 0x00f000f0u};
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+              mma_bf16_16816(o[i * 4 + m], af, pb[p][0], pb[p][1]);
+              if constexpr (PARTS > 1) {
+                const uint32_t mid[4] = {kNeg8, kNeg128, kNeg8, kNeg128};
+                mma_bf16_16816(o[i * 4 + m], mid, pb[p][0], pb[p][1]);
+              }
+            }
           }
         }
-        const uint32_t w4[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const uint32_t x0 = w4[m], x1 = w4[m] >> 8;
-          const uint32_t af[4] = {x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu,
-                                  x1 & 0x00f000f0u};
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) mma_bf16_16816(o[i * 4 + m], af, pb[p][0], pb[p][1]);
-        }
       }
+      __syncwarp();                               // every lane has read the stage
+      if (k + ST < count) issue(k + ST, st);
     }
     if (!ok) {
-      // drain this warp's copies in flight (bounded)
-      while (used != issued) {
-        (void)mbar_wait_bounded(&bars[warp][used % ST], (used / ST) & 1, a.ctrl);
-        ++used;
-      }
+      // wait, within the bound, for this warp's other copies in flight
+      for (int st = 0; st < ST; ++st)
+        if (st != static_cast<int>(used % ST))
+          (void)mbar_wait_bounded(&bars[warp][st], ((used + 1) / ST) & 1, a.ctrl);
+      more = false;
+    } else {
+      more = next_piece(s_done[(piece + 1) & 1]);
     }
-    if (x_end == part1) grid_launch_dependents();
-    if (!__syncthreads_and(ok)) return;
-
-    // ---- the warps' results, merged in shared memory (the ring is idle)
+    if (!more) grid_launch_dependents();
+    // ---- the warps' results, merged in shared memory
     l0 += __shfl_xor_sync(0xffffffffu, l0, 4);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 8);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 16);
@@ -484,94 +675,99 @@ __global__ void __launch_bounds__(kKv4Warps * 32, sizeof(T) == 2 ? 2 : 1)
         zo0[i] += __shfl_xor_sync(0xffffffffu, zo0[i], m);
         zo1[i] += __shfl_xor_sync(0xffffffffu, zo1[i], m);
       }
+      zo0[i] *= 1.f / kUp;
+      zo1[i] *= 1.f / kUp;
     }
     constexpr int OR = merge_row(D);
-    float* sm = reinterpret_cast<float*>(ring);
+    float* sm = reinterpret_cast<float*>(ring + C::kRing);
     float* sm_o = sm;                             // [NW][8][OR]
-    float* sm_m = sm + NW * 8 * OR;               // [NW][8]
+    float* sm_m = sm + NW * 8 * OR;               // [NW][8], then the warps' weights
     float* sm_l = sm_m + NW * 8;
     const int h0 = 2 * cq, h1 = 2 * cq + 1;
     if (gq == 0) {
-      sm_m[warp * 8 + h0] = m0; sm_l[warp * 8 + h0] = l0;
-      sm_m[warp * 8 + h1] = m1; sm_l[warp * 8 + h1] = l1;
+      sm_m[warp * 8 + h0] = 64.f - n0; sm_l[warp * 8 + h0] = l0 * (1.f / kUp);
+      sm_m[warp * 8 + h1] = 64.f - n1; sm_l[warp * 8 + h1] = l1 * (1.f / kUp);
     }
     if (h0 < a.G) {
       // rows gq + 8 hold codes read 16 times too large
 #pragma unroll
       for (int i = 0; i < NG * 4; ++i) {
         const int ch = i * 16 + gq;
-        sm_o[(warp * 8 + h0) * OR + ch] = fmaf(o[i][0], kDown, zo0[i / 4]);
-        sm_o[(warp * 8 + h1) * OR + ch] = fmaf(o[i][1], kDown, zo1[i / 4]);
-        sm_o[(warp * 8 + h0) * OR + ch + 8] = fmaf(o[i][2], kDown * 0.0625f, zo0[i / 4]);
-        sm_o[(warp * 8 + h1) * OR + ch + 8] = fmaf(o[i][3], kDown * 0.0625f, zo1[i / 4]);
+        const float c0 = kMid * ones[i / 4][0], c1 = kMid * ones[i / 4][1];   // (0 for fp32)
+        sm_o[(warp * 8 + h0) * OR + ch] = fmaf(o[i][0] - c0, kDown, zo0[i / 4]);
+        sm_o[(warp * 8 + h1) * OR + ch] = fmaf(o[i][1] - c1, kDown, zo1[i / 4]);
+        sm_o[(warp * 8 + h0) * OR + ch + 8] = fmaf(fmaf(o[i][2], 0.0625f, -c0), kDown, zo0[i / 4]);
+        sm_o[(warp * 8 + h1) * OR + ch + 8] = fmaf(fmaf(o[i][3], 0.0625f, -c1), kDown, zo1[i / 4]);
       }
     }
+    if (!__syncthreads_and(ok)) {
+      // the copies of a next piece that a warp began end before it leaves
+      if (more)
+        for (int k = 0; k < count && k < ST; ++k)
+          (void)mbar_wait_bounded(&bars[warp][(used + k) % ST], ((used + k) / ST) & 1, a.ctrl);
+      return;
+    }
+    if (warp < 8) {                               // head `warp`: lane w holds warp w's (m, l)
+      const float m = lane < NW ? sm_m[lane * 8 + warp] : -INFINITY;
+      const float mx = warp_max_xor(m, 16, 1);
+      const float w = m == -INFINITY ? 0.f : ex2_ftz(m - mx);
+      float l = lane < NW ? w * sm_l[lane * 8 + warp] : 0.f;
+#pragma unroll
+      for (int i = 16; i >= 1; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+      __syncwarp();
+      if (lane < NW) sm_m[lane * 8 + warp] = w;
+      if (lane == 0) { s_mx[warp] = mx; s_l[warp] = l; }
+    }
     __syncthreads();
-    const bool whole = x == u0 && x_end == u1;
-    // slot 0: the part's first piece, slot 1: its last one
-    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (x == part0 ? 0 : 1);
+    const Kv4Done dn = s_done[piece & 1];
     T* out = static_cast<T*>(a.out);
     for (int i = threadIdx.x; i < a.G * D; i += NW * 32) {
       const int h = i / D, ch = i % D;
-      float mx = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm_m[w * 8 + h]);
-      float v = 0.f, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float mw = sm_m[w * 8 + h];
-        const float sc = mw == -INFINITY ? 0.f : exp2f(mw - mx);
-        v = fmaf(sc, sm_o[(w * 8 + h) * OR + ch], v);
-        l = fmaf(sc, sm_l[w * 8 + h], l);
-      }
-      if (whole) {
-        out[(head0 + h) * D + ch] = Dt<T>::from_f(v / l);
+      float v = 0.f;
+#pragma unroll 4
+      for (int w = 0; w < NW; ++w) v = fmaf(sm_m[w * 8 + h], sm_o[(w * 8 + h) * OR + ch], v);
+      if (dn.slot < 0) {
+        out[(dn.bh * a.G + h) * D + ch] = Dt<T>::from_f(v / s_l[h]);
         if (a.lse != nullptr && ch == 0)
-          a.lse[head0 + h] = (mx + log2f(l)) * 0.69314718055994531f;
+          a.lse[dn.bh * a.G + h] = (s_mx[h] + log2f(s_l[h])) * 0.69314718055994531f;
       } else {
-        a.part_o[(slot * a.G + h) * D + ch] = v;
+        a.part_o[(static_cast<int64_t>(dn.slot) * a.G + h) * D + ch] = v;
         if (ch == 0) {
-          a.part_ml[(slot * a.G + h) * 2] = mx;
-          a.part_ml[(slot * a.G + h) * 2 + 1] = l;
+          a.part_ml[(dn.slot * a.G + h) * 2] = s_mx[h];
+          a.part_ml[(dn.slot * a.G + h) * 2 + 1] = s_l[h];
         }
       }
     }
     __syncthreads();
-    if (!whole) {
-      if (threadIdx.x == 0) {
-        const int parts = kv4_owner(total, ctas, u1 - 1) - kv4_owner(total, ctas, u0) + 1;
-        s_last = atomic_add_acq_rel(a.counters + bh, 1) == parts - 1;
-      }
+    if (dn.slot >= 0) {
+      if (threadIdx.x == 0)
+        s_last = atomic_add_acq_rel(a.counters + dn.bh, 1) == dn.parts - 1;
       __syncthreads();
       if (s_last) {
-        kv4_merge<T, D>(a, sm, total, ctas, u0, u1, head0);
-        if (threadIdx.x == 0) a.counters[bh] = 0;
+        kv4_merge<T, D>(a, sm, dn.first, dn.parts, dn.late != 0, dn.bh * a.G);
+        if (threadIdx.x == 0) a.counters[dn.bh] = 0;
       }
       __syncthreads();
     }
-    // the next piece's copies overwrite what was just read here
-    fence_proxy_async_smem();
-    __syncthreads();
-    x = x_end;
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool SEL>
 static cudaError_t kv4_attend_t(const Shape& s, const Kv4K& k, int ctas, cudaStream_t st) {
-  using C = Kv4Cfg<D>;
+  using C = Kv4Cfg<T, D>;
   static std::atomic<bool> attr_set[64];   // per device; launches may come from several host threads
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<T, D>,
+    cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<T, D, SEL>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kKv4Warps * 32);
+  cfg.blockDim = dim3(kKv4Warps<T> * 32);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -579,18 +775,42 @@ static cudaError_t kv4_attend_t(const Shape& s, const Kv4K& k, int ctas, cudaStr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_attend_kernel<T, D>, k);
+  return cudaLaunchKernelEx(&cfg, kv4_attend_kernel<T, D, SEL>, k);
 }
 
-// CTAs of a launch: one wave (two CTAs per SM for bf16, one for fp32), at most
-// kMaxSplits per (row, KV head), none with less than kKv4MinBlocks blocks.
-int kv4_ctas(const Shape& s, int64_t blocks_bound, int num_sms) {
+template <typename T, int D>
+static cudaError_t kv4_attend_d(const Shape& s, const Kv4K& k, int ctas, cudaStream_t st) {
+  return k.sel != nullptr ? kv4_attend_t<T, D, true>(s, k, ctas, st)
+                          : kv4_attend_t<T, D, false>(s, k, ctas, st);
+}
+
+// CTAs of a launch over at most blocks_bound blocks per (row, KV head): one per
+// SM at most, none with less than kKv4MinBlocks blocks where there are more.
+// *splits > 0: that many parts of every (row, head); 0: parts of the range.
+// A cut of every unit alike leaves up to units - 1 SMs idle; it is taken where
+// at least nine tenths of them work (a CTA that crosses from one unit to
+// another pays a second piece's fixed cost, about a tenth of a 128K context).
+int kv4_ctas(const Shape& s, int64_t blocks_bound, bool ragged, int num_sms, int* splits) {
   const int64_t units = static_cast<int64_t>(s.B) * s.H;
-  int64_t n = static_cast<int64_t>(num_sms) * (s.bf16 ? 2 : 1);
-  if (n > kKv4MaxCtas) n = kKv4MaxCtas;
-  if (n > units * kMaxSplits) n = units * kMaxSplits;
-  const int64_t most = (units * blocks_bound + kKv4MinBlocks - 1) / kKv4MinBlocks;
-  return static_cast<int>(n < most ? n : most);
+  const int64_t want = (blocks_bound + kKv4MinBlocks - 1) / kKv4MinBlocks;   // parts of one unit
+  const int64_t sms = num_sms < kKv4MaxCtas ? num_sms : kKv4MaxCtas;
+  int64_t S = units > sms ? 0 : sms / units;
+  if (S > want) S = want;
+  if (S > kMaxSplits) S = kMaxSplits;
+  if (!ragged && S > 0 && (S == want || S == kMaxSplits || units * S * 10 >= sms * 9)) {
+    *splits = static_cast<int>(S);
+    return static_cast<int>(units * S);
+  }
+  *splits = 0;
+  int64_t n = units * (want < kMaxSplits ? want : kMaxSplits);
+  return static_cast<int>(n < sms ? n : sms);
+}
+
+// most CTAs of any launch up to blocks_bound blocks, on any device
+int kv4_most_ctas(const Shape& s, int64_t blocks_bound) {
+  const int64_t want = (blocks_bound + kKv4MinBlocks - 1) / kKv4MinBlocks;
+  const int64_t n = static_cast<int64_t>(s.B) * s.H * (want < kMaxSplits ? want : kMaxSplits);
+  return static_cast<int>(n < kKv4MaxCtas ? n : kKv4MaxCtas);
 }
 
 cudaError_t launch_kv4_attend(const Shape& s, const Kv4Args& a, cudaStream_t st) {
@@ -598,13 +818,12 @@ cudaError_t launch_kv4_attend(const Shape& s, const Kv4Args& a, cudaStream_t st)
   k.q = a.q; k.kv4 = static_cast<const uint8_t*>(a.kv4); k.sel = a.sel; k.lens = a.lens;
   k.part_o = a.part_o; k.part_ml = a.part_ml; k.counters = a.counters; k.ctrl = a.ctrl;
   k.out = a.out; k.lse = a.lse; k.len = a.len; k.r = a.r; k.n_min = a.n_min;
-  k.B = s.B; k.H = s.H; k.G = s.G; k.Hq = s.Hq; k.Mmax = s.Mmax; k.n_sel = a.n_sel;
+  k.B = s.B; k.H = s.H; k.G = s.G; k.splits = a.splits; k.Mmax = s.Mmax; k.n_sel = a.n_sel;
   k.scale_log2 = a.scale * 1.4426950408889634f;
-  if (s.bf16)
-    return s.D == 128 ? kv4_attend_t<__nv_bfloat16, 128>(s, k, a.ctas, st)
-                      : kv4_attend_t<__nv_bfloat16, 64>(s, k, a.ctas, st);
-  return s.D == 128 ? kv4_attend_t<float, 128>(s, k, a.ctas, st)
-                    : kv4_attend_t<float, 64>(s, k, a.ctas, st);
+  if (s.bf16) return s.D == 128 ? kv4_attend_d<__nv_bfloat16, 128>(s, k, a.ctas, st)
+                                : kv4_attend_d<__nv_bfloat16, 64>(s, k, a.ctas, st);
+  return s.D == 128 ? kv4_attend_d<float, 128>(s, k, a.ctas, st)
+                    : kv4_attend_d<float, 64>(s, k, a.ctas, st);
 }
 
 }  // namespace resa

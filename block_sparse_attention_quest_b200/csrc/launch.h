@@ -185,12 +185,14 @@ struct Kv4Args {
   Ctrl* ctrl;
   void* out;
   float* lse;
-  int ctas;               // kv4_ctas
+  int ctas, splits;       // kv4_ctas
 };
 cudaError_t launch_kv4_attend(const Shape& s, const Kv4Args& a, cudaStream_t st);
 constexpr int kKv4MaxCtas = 512;
-// CTAs of a launch over at most blocks_bound blocks per (row, KV head)
-int kv4_ctas(const Shape& s, int64_t blocks_bound, int num_sms);
+// CTAs of a launch over at most blocks_bound blocks per (row, KV head); ragged:
+// with per-row lengths
+int kv4_ctas(const Shape& s, int64_t blocks_bound, bool ragged, int num_sms, int* splits);
+int kv4_most_ctas(const Shape& s, int64_t blocks_bound);
 
 // bounded wait of one thread until *flag >= target (failure-detection check)
 cudaError_t launch_wait_check(const int* flag, int target, unsigned long long limit_ns,

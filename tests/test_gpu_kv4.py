@@ -195,10 +195,14 @@ def run_dense(resa, B, H, G, d, dtype, lens, cap, seed=5, bound=None, stale=True
     assert resa.workspace_status(ws) == resa.RESA_OK
     check(resa, q, clean, lens, None, out.double().cpu().numpy(), lse.double().cpu().numpy(), scale,
           dtype, d, H)
+    again = torch.empty_like(out)
+    resa.decode_dense_kv4(qt, None, None, rec, None, bound, scale, again, ws, lens=lt)
+    assert torch.equal(again, out)                     # no order of arrival shows
     if len(set(lens)) == 1 and bound == lens[0]:
-        again = torch.empty_like(out)
-        resa.decode_dense_kv4(qt, None, None, rec, None, bound, scale, again, ws)
-        assert torch.equal(again, out)
+        # without lengths (another cut of the work): the same bounds
+        resa.decode_dense_kv4(qt, None, None, rec, None, bound, scale, again, ws, lse=lse)
+        check(resa, q, clean, lens, None, again.double().cpu().numpy(), lse.double().cpu().numpy(),
+              scale, dtype, d, H)
     return args, out
 
 
