@@ -321,12 +321,6 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
   int i0, i1, count, tail, part_block, blocks_r, ids = -1, ids_now = -1;
   int64_t bh;
   const uint8_t* base;
-  constexpr int QW = sizeof(T);                   // 16-byte words of 16 channels
-  uint4 qraw[NG][QW];                             // head gq's channels 64 g + 16 cq .. + 15
-#pragma unroll
-  for (int i = 0; i < NG; ++i)
-#pragma unroll
-    for (int j = 0; j < QW; ++j) qraw[i][j] = make_uint4(0u, 0u, 0u, 0u);
   // With a list, lane u of `ids` holds entry u % 2 of this warp's pair
   // 16 w + u / 2 around the pair copied next, `ids_now` those around the pair
   // in use; pair k is entries i0 + 2 (warp + k NW) and the next.
@@ -415,15 +409,6 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     tail = static_cast<int>(len_r & (kBlock - 1));
     part_block = tail ? blocks_r - 1 : -2;
     base = a.kv4 + bh * a.Mmax * REC;
-    // (ahead of the copies, which it would queue behind)
-    if (gq < a.G) {
-      const T* qg = static_cast<const T*>(a.q) + (bh * a.G + gq) * D + cq * 16;
-#pragma unroll
-      for (int i = 0; i < NG; ++i)
-#pragma unroll
-        for (int j = 0; j < QW; ++j)
-          qraw[i][j] = ldg16(reinterpret_cast<const uint4*>(qg + i * 64) + j);
-    }
     const int pairs = (i1 - i0 + 1) / 2;
     count = pairs > warp ? (pairs - warp + NW - 1) / NW : 0;
     for (int k = 0; k < count && k < ST; ++k) issue(k, (used + k) % ST);
@@ -438,6 +423,7 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     uint32_t qb[PARTS][NG * 4][2];
     float qs0[NG], qs1[NG];
     {
+      const T* qg = static_cast<const T*>(a.q) + bh * a.G * D;
 #pragma unroll
       for (int g2 = 0; g2 < NG; ++g2) {
         float sum = 0.f;
@@ -445,8 +431,8 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
         for (int j = 0; j < 2; ++j) {
           float f[8];
 #pragma unroll
-          for (int i = 0; i < QW / 2; ++i)
-            Chunk<T>::unpack(qraw[g2][j * (QW / 2) + i], f + i * Chunk<T>::N);
+          for (int i = 0; i < 8; ++i) f[i] = 0.f;
+          if (gq < a.G) load8<T>(qg + gq * D + g2 * 64 + cq * 16 + j * 8, f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum += f[i];
           float part[8][PARTS];
