@@ -46,7 +46,7 @@ EXPORTED = ("resa_num_selected", "resa_workspace_bytes", "resa_build_desc",
            "resa_kv4_bytes", "resa_kv4_workspace_bytes", "resa_kv4_quantize",
            "resa_kv4_dequantize", "resa_decode_dense_kv4", "resa_decode_sparse_kv4",
            "resa_attend_blocks_kv4", "resa_weights_workspace_bytes",
-           "resa_decode_dense_weights", "resa_evict")
+           "resa_decode_dense_weights", "resa_evict", "resa_prefill_packed")
 
 
 class Dims(ctypes.Structure):
@@ -129,6 +129,10 @@ _lib.resa_evict.restype = ctypes.c_int
 _lib.resa_evict.argtypes = [ctypes.POINTER(Dims), _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int32,
                             ctypes.c_int32, ctypes.c_int64, _P, _P, _P, _P, _P, _P,
                             ctypes.c_size_t, _P]
+_lib.resa_prefill_packed.restype = ctypes.c_int
+_lib.resa_prefill_packed.argtypes = [ctypes.POINTER(Dims), _P, _P, _P, _P, ctypes.c_int64,
+                                     ctypes.c_int64, _P, _P, _P, ctypes.c_float, _P, _P,
+                                     ctypes.c_size_t, _P]
 _lib.resa_wait_check.restype = ctypes.c_int
 _lib.resa_wait_check.argtypes = [_P, ctypes.c_int32, ctypes.c_uint32, _P, _P]
 _lib.resa_workspace_status.restype = ctypes.c_int
@@ -331,6 +335,26 @@ def prefill(q, k_cache, v_cache, desc, length: int, softmax_scale: float, out, w
     _check(_lib.resa_prefill(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(desc),
                              int(length), float(softmax_scale), _ptr(out), _ptr(workspace),
                              workspace.numel(), _stream(stream)), "resa_prefill")
+
+
+def prefill_packed(q, k, v, starts, longest: int, k_cache, v_cache, desc, softmax_scale: float,
+                   out, workspace, stream=None) -> None:
+    """Causal attention over packed prompts (q, out: [total, Hq, d]; k, v:
+    [total, Hkv, d]; starts: int32 CUDA tensor [batch + 1]), which also fills
+    rows of k_cache and v_cache [batch, Hkv, max_len, d] and desc (or None)."""
+    dims = dims_for(k_cache, q.shape[1])
+    if (tuple(k.shape) != (q.shape[0], k_cache.shape[1], q.shape[2]) or v.shape != k.shape
+            or out.shape != q.shape or k_cache.shape != v_cache.shape
+            or q.shape[2] != k_cache.shape[3]):
+        raise ValueError("q, out must be [total, n_q_heads, d] and k, v [total, n_kv_heads, d]")
+    if any(t.dtype != k_cache.dtype for t in (q, k, v, v_cache, out)):
+        raise ValueError("q, k, v, out and the caches must share a dtype")
+    if _lens(starts) is None or starts.numel() != k_cache.shape[0] + 1:
+        raise ValueError("starts must be int32 [batch + 1]")
+    _check(_lib.resa_prefill_packed(
+        ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(starts), int(q.shape[0]), int(longest),
+        _ptr(k_cache), _ptr(v_cache), _ptr(desc), float(softmax_scale), _ptr(out),
+        _ptr(workspace), workspace.numel(), _stream(stream)), "resa_prefill_packed")
 
 
 # ---- attention weights (float32 [B, H_kv, max_len] running sums) and eviction

@@ -13,7 +13,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libresa.so")
 SOURCES = ["api.cu", "desc.cu", "select.cu", "attend.cu", "rectify_tc.cu", "noalloc.cu", "decode_coop.cu",
-           "kv4_cache.cu", "kv4_attend.cu", "evict.cu"]
+           "kv4_cache.cu", "kv4_attend.cu", "evict.cu", "prefill_packed.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

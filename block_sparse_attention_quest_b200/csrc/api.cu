@@ -105,6 +105,23 @@ bool make_query_map(CUtensorMap* m, const void* base, const Shape& s, int f) {
   return r == CUDA_SUCCESS;
 }
 
+// 3-D view [T][heads][D] of packed bf16 rows, (64 x box_heads x box_rows)
+// boxes, 128-byte swizzle
+bool make_packed_map(CUtensorMap* m, const void* base, int D, int heads, int T, int box_heads,
+                     int box_rows) {
+  auto enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(T)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(heads) * D * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool rectify_on_tensor_cores(const Shape& s) {
   return s.bf16 && (s.G == 1 || s.G == 2 || s.G == 4 || s.G == 8);
 }
@@ -593,6 +610,52 @@ int resa_prefill(const resa_dims* dims, const void* q, const void* k_cache, cons
   return cuda_status(launch_rectify_tc(r, static_cast<cudaStream_t>(stream)));
 }
 
+// ---- packed prompts
+
+// whether [a, a + n) and [b, b + m) share a byte
+static bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + m && y < x + n;
+}
+
+int resa_prefill_packed(const resa_dims* dims, const void* q, const void* k, const void* v,
+                        const int32_t* starts, int64_t total, int64_t longest, void* k_cache,
+                        void* v_cache, void* desc, float softmax_scale, void* out,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  Shape s;
+  const int rc = check_dims(dims, &s);
+  if (rc != RESA_OK) return rc;
+  if (!q || !k || !v || !out || !workspace || !lens_ok(starts) ||
+      (k_cache == nullptr) != (v_cache == nullptr) || !aligned16(q) || !aligned16(k) ||
+      !aligned16(v) || !aligned16(out) || (k_cache && (!aligned16(k_cache) || !aligned16(v_cache))) ||
+      (desc && !aligned16(desc)) || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
+      total < 1 || longest < 1 || !(std::isfinite(softmax_scale) && softmax_scale > 0.f))
+    return RESA_ERR_INVALID_ARG;
+  if (!s.bf16) return RESA_ERR_UNSUPPORTED;
+  if (longest > s.L_max) return RESA_ERR_CAPACITY;
+  if (workspace_bytes < kCtrlBytes) return RESA_ERR_WORKSPACE;
+  int Gt = 1;
+  while (Gt < 8 && s.G % (2 * Gt) == 0) Gt *= 2;
+  const int64_t ctas = (total / (256 / Gt) + s.B) * (s.Hq / Gt);
+  if (total > 2147483647LL - 512 || ctas > 2147483647LL) return RESA_ERR_UNSUPPORTED;
+  // a CTA reads keys and values of tokens that other CTAs' outputs follow
+  const size_t qb = static_cast<size_t>(total) * s.Hq * s.D * 2, kb = qb / s.G;
+  if (overlap(out, qb, q, qb) || overlap(out, qb, k, kb) || overlap(out, qb, v, kb))
+    return RESA_ERR_INVALID_ARG;
+  PackedArgs r{};
+  r.B = s.B; r.T = static_cast<int>(total); r.longest = static_cast<int>(longest < total ? longest : total);
+  r.Hq = s.Hq; r.H = s.H; r.G = s.G; r.Gt = Gt; r.D = s.D; r.L_max = s.L_max;
+  r.scale = softmax_scale; r.starts = starts; r.k = k; r.v = v; r.k_cache = k_cache;
+  r.v_cache = v_cache; r.desc = desc; r.out = out; r.ctrl = reinterpret_cast<Ctrl*>(workspace);
+  CUtensorMap tq, tk, tv;
+  if (!make_packed_map(&tq, q, s.D, s.Hq, r.T, Gt, 128 / Gt) ||
+      !make_packed_map(&tk, k, s.D, s.H, r.T, 1, 128) ||
+      !make_packed_map(&tv, v, s.D, s.H, r.T, 1, 128))
+    return RESA_ERR_CUDA;
+  r.tm_q = &tq; r.tm_k = &tk; r.tm_v = &tv;
+  return cuda_status(launch_prefill_packed(r, static_cast<cudaStream_t>(stream)));
+}
+
 // ---- attention weights and eviction
 
 // ws_layout, then every token's logits and each head's (max, sum)
@@ -641,12 +704,6 @@ int resa_decode_dense_weights(const resa_dims* dims, const void* q, const void* 
                      num_sms, st, false, lens, 0.0, 0, nullptr, logits, ml);
   if (rc != RESA_OK) return rc;
   return cuda_status(launch_add_weights(s, logits, ml, weights, len, lens, k_new != nullptr, st));
-}
-
-// whether [a, a + n) and [b, b + m) share a byte
-static bool overlap(const void* a, size_t n, const void* b, size_t m) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + m && y < x + n;
 }
 
 int resa_evict(const resa_dims* dims, const void* k_cache, const void* v_cache,

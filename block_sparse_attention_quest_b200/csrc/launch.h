@@ -137,6 +137,26 @@ struct RectArgs {
 cudaError_t launch_rectify_tc(const RectArgs& r, cudaStream_t st);
 int attend_ctas_per_sm(const Shape& s);
 
+// packed prompts (bf16; prefill_packed.cu) -----------------------------------------
+struct PackedArgs {
+  int B, T, longest;      // sequences, packed tokens, bound on a sequence's length
+  int Hq, H, G, Gt, D;    // Gt: query heads of one tile (a power of two that divides G)
+  int64_t L_max;
+  float scale;
+  const int32_t* starts;  // [B + 1]
+  const void* k;          // packed keys and values [T][H][D] (for the caches)
+  const void* v;
+  void* k_cache;          // both or neither
+  void* v_cache;
+  void* desc;             // or nullptr
+  void* out;              // [T][Hq][D]
+  Ctrl* ctrl;
+  const CUtensorMap* tm_q;  // q as [T][Hq][D], 64 x Gt x (128 / Gt) boxes
+  const CUtensorMap* tm_k;  // k as [T][H][D], 64 x 1 x 128 boxes
+  const CUtensorMap* tm_v;
+};
+cudaError_t launch_prefill_packed(const PackedArgs& r, cudaStream_t st);
+
 // attention weights and eviction (evict.cu) ---------------------------------------
 // weights[b][g][t] += sum over the group's heads of 2^(logit - m) / l; with
 // `fresh` the newest token's sum starts at this step

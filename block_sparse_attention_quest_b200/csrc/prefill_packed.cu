@@ -1,0 +1,515 @@
+// Causal attention over packed prompts of different lengths on the 5th
+// generation tensor cores, filling the caches and block descriptors that
+// decoding starts from.
+//
+//   out_i = sum_{t <= i} softmax_t(scale q_i . k_t) v_t   inside each sequence
+//
+// Sequence b is tokens starts[b] .. starts[b + 1] - 1 of q, k and v. A CTA
+// takes 256 rows of one sequence: 256 / Gt consecutive queries of Gt query
+// heads that share a KV head (Gt: the largest power of two that divides the
+// group), as two 128-row tiles A and B (M = 128, row = query * Gt + head,
+// which is how q lies in memory), and walks the key tiles of 128 tokens up to
+// its last query. Both tiles use every K and V tile that arrives, so a tile is
+// read from L2 once for 256 rows. Bound: the tensor cores and, equally, the
+// exponential unit (2 x 128 x 128 exponentials take 2048 cycles of an SM, as
+// do the four 128^3 products).
+//
+// 12 warps:
+//   0-3, 4-7  softmax of tile A and of tile B, one row per thread (= TMEM
+//             lane): S is read into registers whole, the row maximum moves
+//             its reference only when it grows by more than 2^8 (O is
+//             rescaled in TMEM then), and P = 2^(s - m) goes back as bf16
+//             over the S columns, as the A operand of the second product;
+//   8         one thread issues the products. For each tile the next S is
+//             issued right behind the O product that reads the previous P
+//             from the same columns: the tensor pipe runs them in order. Its
+//             completion therefore also says that O may be rescaled;
+//   9         one thread issues the TMA copies: Q, then K and V tiles through a
+//             ring of five 128-token slots;
+//   10        copies this CTA's own tokens of K and V from the packed tensors to the
+//             caches and writes their block descriptors (one CTA per KV head);
+//   11        idle (registers are handed over by whole warpgroups).
+// While one tile's softmax runs, the other tile's products do.
+//
+// Rows of a key tile past the sequence's end belong to other sequences: their
+// scores are masked and their V rows zeroed in shared memory, so nothing of
+// another sequence (an infinity times 0) reaches an output.
+#include "launch.h"
+#include "tc.cuh"
+
+namespace resa {
+
+struct PackedK {
+  __nv_bfloat16* out;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const int32_t* starts;      // [B + 1]
+  __nv_bfloat16* k_cache;     // or nullptr
+  __nv_bfloat16* v_cache;
+  __nv_bfloat16* desc;        // or nullptr
+  Ctrl* ctrl;
+  int64_t L_max;
+  int Mmax;
+  int B, T, longest, Hq, H, G, Gt;
+  float scale_log2;
+};
+
+template <int D>
+struct PackedCfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kHalfBytes = 128 * 128;          // [128 rows][64 bf16]
+  static constexpr int kTileBytes = kHalves * kHalfBytes;
+  static constexpr int kSlots = 5;
+  // (at least 116 KB: a second CTA on the SM would wait for TMEM columns)
+  static constexpr int kNeed = (2 + kSlots) * kTileBytes + 1024;
+  static constexpr int kSmem = kNeed > 116 * 1024 ? kNeed : 116 * 1024;
+  // twelve warps start with 168 registers each; the softmax warps, which hold
+  // a row of S, take 208, the third warpgroup leaves them (2 * 208 + 88 = 3 * 168)
+  static constexpr int kThreads = 12 * 32;
+  static constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+};
+
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// bounds of sequence b, and whether the starts given are out of order or range
+struct SeqBounds {
+  int begin, len;
+  bool bad;
+};
+__device__ __forceinline__ SeqBounds seq_bounds(const PackedK& a, int b) {
+  const int s0 = a.starts[b], s1 = a.starts[b + 1];
+  SeqBounds r;
+  r.begin = s0 < 0 ? 0 : (s0 > a.T ? a.T : s0);
+  const int end = s1 < r.begin ? r.begin : (s1 > a.T ? a.T : s1);
+  r.len = end - r.begin > a.longest ? a.longest : end - r.begin;
+  r.bad = r.begin != s0 || r.begin + r.len != s1;
+  return r;
+}
+
+// K and V rows [t0, t0 + n) of a sequence to its cache row, and the
+// descriptors of their blocks (t0 is a multiple of 16); one warp.
+template <int D>
+__device__ __forceinline__ void fill_cache(const PackedK& a, int b, int begin, int g, int t0,
+                                           int n) {
+  constexpr int CPR = D / 8, TPP = 32 / CPR, NP = kBlock / TPP;
+  const int lane = threadIdx.x & 31, chunk = lane % CPR, r0 = lane / CPR;
+  const int64_t bh = static_cast<int64_t>(b) * a.H + g;
+  const int64_t stride = static_cast<int64_t>(a.H) * D;
+  const __nv_bfloat16* ks = a.k + (static_cast<int64_t>(begin + t0) * a.H + g) * D + chunk * 8;
+  const __nv_bfloat16* vs = a.v + (static_cast<int64_t>(begin + t0) * a.H + g) * D + chunk * 8;
+#pragma unroll 1
+  for (int j = 0; j < n; j += kBlock) {
+    const int valid = n - j < kBlock ? n - j : kBlock;
+    uint4 x[NP];
+    if (a.v_cache != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        if (r0 + i * TPP < valid) x[i] = ldg16(vs + (j + r0 + i * TPP) * stride);
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        if (r0 + i * TPP < valid)
+          *reinterpret_cast<uint4*>(a.v_cache + (bh * a.L_max + t0 + j + r0 + i * TPP) * D +
+                                    chunk * 8) = x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      if (r0 + i * TPP < valid) x[i] = ldg16(ks + (j + r0 + i * TPP) * stride);
+    float mn[8], mx[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) { mn[e] = INFINITY; mx[e] = -INFINITY; }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if (r0 + i * TPP < valid) {
+        if (a.k_cache != nullptr)
+          *reinterpret_cast<uint4*>(a.k_cache + (bh * a.L_max + t0 + j + r0 + i * TPP) * D +
+                                    chunk * 8) = x[i];
+        float f[8];
+        Chunk<__nv_bfloat16>::unpack(x[i], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) { mn[e] = fminf(mn[e], f[e]); mx[e] = fmaxf(mx[e], f[e]); }
+      }
+    }
+    if (a.desc == nullptr) continue;
+#pragma unroll
+    for (int m = CPR; m < 32; m <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        mn[e] = fminf(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], m));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], m));
+      }
+    if (lane < CPR) {
+      __nv_bfloat16* d = a.desc + (bh * a.Mmax + (t0 + j) / kBlock) * 2 * D + chunk * 8;
+      *reinterpret_cast<uint4*>(d) = Chunk<__nv_bfloat16>::pack(mn);
+      *reinterpret_cast<uint4*>(d + D) = Chunk<__nv_bfloat16>::pack(mx);
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
+    prefill_packed_kernel(const __grid_constant__ CUtensorMap tmQ,
+                          const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, PackedK a) {
+  using C = PackedCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_q[2], bar_full[C::kSlots], bar_empty[C::kSlots];
+  __shared__ __align__(8) uint64_t bar_s[2], bar_p[2], bar_o[2];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int s_seq, s_block;
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  auto sQ = [&](int w) { return base + w * C::kTileBytes; };
+  auto slot = [&](int n) { return base + (2 + n % C::kSlots) * C::kTileBytes; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int QT = 128 / a.Gt, QB = 2 * QT;         // queries per tile, per CTA
+  const int n_hg = a.Hq / a.Gt;
+  const int hg = blockIdx.x % n_hg, x = blockIdx.x / n_hg;
+
+  // which sequence and which of its query blocks (the last ones, which see the
+  // most keys, first)
+  if (warp == 0) {
+    int run = 0, seq = -1, blk = 0;
+    for (int b0 = 0; b0 < a.B && seq < 0; b0 += 32) {
+      const int b = b0 + lane;
+      int n = 0;
+      if (b < a.B) {
+        const SeqBounds sb = seq_bounds(a, b);
+        n = (sb.len + QB - 1) / QB;
+        if (blockIdx.x == 0 && sb.bad) raise_error(a.ctrl, kErrBadIndex);
+      }
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const bool here = x >= run + inc - n && x < run + inc;
+      const unsigned who = __ballot_sync(0xffffffffu, here);
+      if (who) {
+        const int src = __ffs(who) - 1;
+        seq = b0 + src;
+        blk = __shfl_sync(0xffffffffu, run + inc - 1 - x, src);
+      }
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    // (the first CTA looks at every entry, to report a bad one)
+    if (blockIdx.x == 0)
+      for (int b = lane; b < a.B; b += 32)
+        if (seq_bounds(a, b).bad) raise_error(a.ctrl, kErrBadIndex);
+    if (lane == 0) { s_seq = seq; s_block = blk; }
+  }
+  __syncthreads();
+  const int b = s_seq;
+  if (b < 0) return;                              // more CTAs than query blocks
+  const SeqBounds sb = seq_bounds(a, b);
+  const int q0 = s_block * QB;
+  const int nq = sb.len - q0 < QB ? sb.len - q0 : QB;
+  const int g = hg * a.Gt / a.G;                  // KV head
+  // key tiles of A and of B (none without queries)
+  const int nt_a = (q0 + (nq < QT ? nq : QT) - 1) / 128 + 1;
+  const int nt_b = nq > QT ? (q0 + nq - 1) / 128 + 1 : 0;
+  const int n_tiles = nt_b > nt_a ? nt_b : nt_a;
+
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&bar_q[w], 1);
+      mbar_init(&bar_s[w], 1);
+      mbar_init(&bar_p[w], 128);
+      mbar_init(&bar_o[w], 1);
+    }
+#pragma unroll
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&bar_full[i], 1);
+      mbar_init(&bar_empty[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 8) tc::alloc(&tmem_base_sh, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_base_sh;
+  auto tS = [&](int w) { return tmem + 128u * w; };
+  auto tO = [&](int w) { return tmem + 256u + 128u * w; };
+
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
+  if (warp == 9) {
+    // ---------------------------------------------------------------- copies
+    if (lane == 0) {
+      prefetch_tmap(&tmQ);
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+      auto load_q = [&](int w) {
+        mbar_arrive_expect_tx(&bar_q[w], C::kTileBytes);
+#pragma unroll
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tma_load_3d(sQ(w) + hf * C::kHalfBytes, &tmQ, hf * 64, hg * a.Gt, sb.begin + q0 + w * QT,
+                      &bar_q[w]);
+      };
+      load_q(0);
+      int n = 0;                                   // copy n: K (even) or V (odd) of tile n / 2
+      bool ok = true;
+      for (; n < 2 * n_tiles; ++n) {
+        const int i = n % C::kSlots;
+        if (n >= C::kSlots &&
+            !(ok = mbar_wait_bounded(&bar_empty[i], (n / C::kSlots - 1) & 1, a.ctrl)))
+          break;
+        mbar_arrive_expect_tx(&bar_full[i], C::kTileBytes);
+        const CUtensorMap* map = n & 1 ? &tmV : &tmK;
+#pragma unroll
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tma_load_3d(slot(n) + hf * C::kHalfBytes, map, hf * 64, g, sb.begin + (n >> 1) * 128,
+                      &bar_full[i]);
+        if (n == 0 && nt_b > 0) load_q(1);
+      }
+      if (!ok) {
+        // the copies in flight end (within the bound) before this CTA does
+        for (int m = n >= C::kSlots ? n - C::kSlots : 0; m < n; ++m)
+          (void)mbar_wait_bounded(&bar_full[m % C::kSlots], (m / C::kSlots) & 1, a.ctrl);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // -------------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t idS = tc::idesc_bf16(128, 128, false);
+      constexpr uint32_t idO = tc::idesc_bf16(128, D, true);
+      auto qk = [&](int w, int t) {
+        const uint32_t qa = smem_u32(sQ(w)), ka = smem_u32(slot(2 * t));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::kHalfBytes + (kk & 3) * 32;
+          tc::mma_ss(tS(w), tc::smem_desc(qa + off, 16, 1024), tc::smem_desc(ka + off, 16, 1024),
+                     idS, kk > 0);
+        }
+        tc::commit(&bar_s[w]);
+      };
+      auto pv = [&](int w, int t) {
+        const uint32_t va = smem_u32(slot(2 * t + 1));
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_ts(tO(w), tS(w) + 8u * kk, tc::smem_desc(va + kk * 2048, C::kHalfBytes, 1024), idO,
+                     t > 0 || kk > 0);
+      };
+      auto full = [&](int n) {
+        return mbar_wait_bounded(&bar_full[n % C::kSlots], (n / C::kSlots) & 1, a.ctrl);
+      };
+      bool ok = full(0);
+      for (int w = 0; ok && w < (nt_b > 0 ? 2 : 1); ++w) {
+        if (!(ok = mbar_wait_bounded(&bar_q[w], 0, a.ctrl))) break;
+        tc::fence_after_sync();
+        qk(w, 0);
+      }
+      if (ok) tc::commit(&bar_empty[0]);
+      for (int t = 0; ok && t < n_tiles; ++t) {
+        if (!(ok = full(2 * t + 1))) break;
+        for (int w = 0; ok && w < 2; ++w) {
+          const int nt = w == 0 ? nt_a : nt_b;
+          if (t >= nt) continue;
+          if (!(ok = mbar_wait_bounded(&bar_p[w], t & 1, a.ctrl))) break;
+          tc::fence_after_sync();
+          pv(w, t);
+          if (t + 1 == nt) tc::commit(&bar_o[w]);
+          if (t + 1 < nt) {
+            if (!(ok = full(2 * t + 2))) break;
+            tc::fence_after_sync();
+            qk(w, t + 1);
+          }
+        }
+        if (!ok) break;
+        // both tiles have taken V of tile t and K of tile t + 1
+        tc::commit(&bar_empty[(2 * t + 1) % C::kSlots]);
+        if (t + 1 < n_tiles) tc::commit(&bar_empty[(2 * t + 2) % C::kSlots]);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------- caches and descriptors
+    if (hg * a.Gt % a.G == 0 && (a.k_cache != nullptr || a.desc != nullptr))
+      fill_cache<D>(a, b, sb.begin, g, q0, nq);
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+    // --------------------------------------------------------------- softmax
+    const int w = warp >> 2;
+    const int nt = w == 0 ? nt_a : nt_b;
+    const int row = threadIdx.x & 127;             // TMEM lane
+    const int qpos = q0 + w * QT + row / a.Gt;     // causal limit
+    const int qpos_lo = q0 + w * QT;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float sl2 = a.scale_log2;
+    float m_ref = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int t = 0; t < nt; ++t) {
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar_s[w], t & 1, a.ctrl));
+      if (!ok) break;
+      tc::fence_after_sync();
+      float s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc::ld32(tS(w) + lane_off + 32 * c, s[c]);
+      tc::wait_ld();
+      const int key0 = t * 128;
+      if (key0 + 127 > qpos_lo) {                  // (the last tiles only)
+        const int lim = qpos - key0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c * 32 + i > lim) s[c][i] = -INFINITY;
+      }
+      float mp[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mp[j] = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mp[i & 7] = fmaxf(mp[i & 7], fmaxf(s[c][i], s[c + 2][i]));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mp[j] = fmaxf(mp[j], mp[j + 4]);
+      const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sl2;
+      const bool need = mx > m_ref + 8.f;
+      if (__any_sync(0xffffffffu, need)) {
+        const float m_new = need ? mx : m_ref;
+        const float alpha = need ? (m_ref == -INFINITY ? 0.f : ex2_fast(m_ref - m_new)) : 1.f;
+        if (t > 0) {
+          // (this S is complete, and the O product before it with it)
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+            tc::ld16(tO(w) + lane_off + c * 16, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tc::st16f(tO(w) + lane_off + c * 16, o);
+          }
+          tc::wait_st();
+        }
+        l *= alpha;
+        m_ref = m_new;
+      }
+      // (a row with no visible key yet, -inf - -inf, takes weight 0)
+      const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t wd[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float p0 = ex2_fast(fmaf(s[c][2 * e], sl2, nm));
+          const float p1 = ex2_fast(fmaf(s[c][2 * e + 1], sl2, nm));
+          sum[e & 3] += p0 + p1;
+          wd[e] = pack_bf16x2(p0, p1);
+        }
+        tc::st16(tS(w) + lane_off + c * 16, wd);
+      }
+      tc::wait_st();
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (key0 + 128 > sb.len) {
+        // V rows past the sequence's end (both tiles' threads do this: the
+        // product of either may come first)
+        const int n = 2 * t + 1;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar_full[n % C::kSlots],
+                                                       (n / C::kSlots) & 1, a.ctrl));
+        if (!ok) break;
+        if (key0 + row >= sb.len) {
+          uint8_t* vt = slot(n) + row * 128;
+#pragma unroll
+          for (int hf = 0; hf < C::kHalves; ++hf)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4*>(vt + hf * C::kHalfBytes + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      tc::fence_before_sync();
+      mbar_arrive(&bar_p[w]);
+    }
+    if (ok && nt > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar_o[w], 0, a.ctrl));
+      if (ok) {
+        tc::fence_after_sync();
+        // each warp's 32 rows through its part of its tile's query buffer (no
+        // product reads it any more), 16-byte unit j of row r at j ^ (r mod 8)
+        constexpr int NU = D / 8;                  // 16-byte units per row
+        uint4* st = reinterpret_cast<uint4*>(sQ(w)) + (warp & 3) * 32 * NU;
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tc::ld32(tO(w) + lane_off + c * 32, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            st[lane * NU + ((c * 4 + k) ^ (lane & 7))] =
+                make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
+                           pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                           pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                           pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+        }
+        __syncwarp();
+        constexpr int RPI = 32 / NU;               // rows per store instruction
+        const int j = lane % NU;
+#pragma unroll 4
+        for (int it = 0; it < 32 / RPI; ++it) {
+          const int r = it * RPI + lane / NU;
+          const int rt = (warp & 3) * 32 + r;      // row of the tile
+          const int qi = w * QT + rt / a.Gt;
+          if (qi >= nq) continue;
+          const int64_t orow = static_cast<int64_t>(sb.begin + q0 + qi) * a.Hq + hg * a.Gt + rt % a.Gt;
+          *reinterpret_cast<uint4*>(a.out + orow * D + j * 8) = st[r * NU + (j ^ (r & 7))];
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 8) {
+    tc::fence_after_sync();
+    tc::dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+static cudaError_t prefill_packed_t(const PackedArgs& r, cudaStream_t st) {
+  using C = PackedCfg<D>;
+  static std::atomic<bool> attr_set[64];   // per device; launches may come from several host threads
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(prefill_packed_kernel<D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  PackedK k{};
+  k.out = static_cast<__nv_bfloat16*>(r.out);
+  k.k = static_cast<const __nv_bfloat16*>(r.k);
+  k.v = static_cast<const __nv_bfloat16*>(r.v);
+  k.starts = r.starts;
+  k.k_cache = static_cast<__nv_bfloat16*>(r.k_cache);
+  k.v_cache = static_cast<__nv_bfloat16*>(r.v_cache);
+  k.desc = static_cast<__nv_bfloat16*>(r.desc);
+  k.ctrl = r.ctrl;
+  k.L_max = r.L_max; k.Mmax = static_cast<int>(r.L_max / kBlock);
+  k.B = r.B; k.T = r.T; k.longest = r.longest; k.Hq = r.Hq; k.H = r.H; k.G = r.G; k.Gt = r.Gt;
+  k.scale_log2 = r.scale * 1.4426950408889634f;
+  // every sequence has at most one query block that is not full
+  const int QB = 256 / r.Gt;
+  const int64_t blocks = r.T / QB + r.B;
+  prefill_packed_kernel<D><<<static_cast<unsigned>(blocks * (r.Hq / r.Gt)), C::kThreads, C::kSmem, st>>>(
+      *r.tm_q, *r.tm_k, *r.tm_v, k);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prefill_packed(const PackedArgs& r, cudaStream_t st) {
+  return r.D == 128 ? prefill_packed_t<128>(r, st) : prefill_packed_t<64>(r, st);
+}
+
+}  // namespace resa

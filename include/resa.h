@@ -290,6 +290,34 @@ RESA_API int resa_rectify_varlen(const resa_dims* dims, const void* q_f, const v
                                  int32_t f, float softmax_scale, void* out_f, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* Prefill of a ragged batch of prompts, packed one behind the other: causal
+ * attention of every token inside its own sequence, and the caches and block
+ * descriptors that decoding starts from, in one launch.
+ *  - q, out [total][n_q_heads][d]; k, v [total][n_kv_heads][d]; sequence b
+ *    (b < dims.batch) is tokens starts[b] .. starts[b+1]-1, starts being a
+ *    DEVICE int32 array [batch+1], 4-byte aligned; a sequence may be empty;
+ *  - longest >= every sequence's length, longest <= max_len;
+ *  - out[starts[b]+i][h] = softmax_t(scale * q[starts[b]+i][h] .
+ *    k[starts[b]+t][h/G], t <= i) . v; rows of out in no sequence are not
+ *    written;
+ *  - k_cache, v_cache (both or neither NULL): slots [0, length) of row b
+ *    receive the sequence's keys and values;
+ *  - desc (or NULL): descriptors of their blocks, as resa_build_desc writes
+ *    them.
+ * A sequence that begins or ends outside [0, total], ends before it begins or
+ * is longer than `longest` is cut to what fits and raises the
+ * RESA_ERR_BAD_INDEX flag. Sequences must not share tokens. Every key and
+ * value should be finite: one that is not reaches every output of its own
+ * sequence whose 128-token key tile holds it (also through a masked place),
+ * and no other sequence. starts is read on the device only (a captured call
+ * can be replayed on other lengths). out must not overlap q, k or v. bf16
+ * only (RESA_ERR_UNSUPPORTED otherwise); any group up to 8. The workspace only
+ * carries the error word: resa_workspace_bytes(dims, longest, 0) suffices. */
+RESA_API int resa_prefill_packed(const resa_dims* dims, const void* q, const void* k, const void* v,
+                                 const int32_t* starts, int64_t total, int64_t longest,
+                                 void* k_cache, void* v_cache, void* desc, float softmax_scale,
+                                 void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- attention weights and eviction ----
  * A budgeted cache beside the block-sparse one (no counterpart on the pages):
  * decode steps add up how much attention every cached key receives, and
