@@ -700,8 +700,10 @@ int resa_decode_dense_weights(const resa_dims* dims, const void* q, const void* 
   if (k_new &&
       launch_append(s, k_new, v_new, k_cache, v_cache, desc, len, st, lens) != cudaSuccess)
     return RESA_ERR_CUDA;
+  // (as a programmatic dependent of the append, which starts no dependent
+  // early, the attention overlaps only its launch with it)
   rc = run_attention(s, q, 1, len, nullptr, 0, softmax_scale, k_cache, v_cache, out, lse, ws, w,
-                     num_sms, st, false, lens, 0.0, 0, nullptr, logits, ml);
+                     num_sms, st, k_new != nullptr, lens, 0.0, 0, nullptr, logits, ml);
   if (rc != RESA_OK) return rc;
   return cuda_status(launch_add_weights(s, logits, ml, weights, len, lens, k_new != nullptr, st));
 }

@@ -19,54 +19,58 @@ namespace resa {
 
 namespace cg = cooperative_groups;
 
-// Grid (tokens / 256, H, B): one token per thread.
+// Grid (tokens / 1024, H, B), 256 threads; a thread adds the weights of four
+// consecutive tokens, whose logits (four times G values) and sums it requests
+// together.
+template <int G>
 __global__ void __launch_bounds__(256) add_weights_kernel(const float* __restrict__ logits,
                                                           const float* __restrict__ ml,
-                                                          float* __restrict__ weights, int H, int G,
+                                                          float* __restrict__ weights, int H,
                                                           int64_t stride, int64_t L_max,
                                                           int64_t len, const int32_t* lens,
                                                           bool fresh) {
-  __shared__ float s_m[8], s_inv[8];
   grid_dependency_wait();
   grid_launch_dependents();
   const int g = blockIdx.y, b = blockIdx.z;
   const int64_t bh = static_cast<int64_t>(b) * H + g;
-  if (threadIdx.x < G) {
-    const float2 p = __ldcg(reinterpret_cast<const float2*>(ml) + bh * G + threadIdx.x);
-    s_m[threadIdx.x] = p.x;
-    s_inv[threadIdx.x] = 1.f / p.y;
-  }
-  __syncthreads();
   const int64_t len_b = row_len(lens, len, b);
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t t = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (t >= len_b) return;
-  const float* z = logits + (bh * stride + t) * G;
-  float x[8];
-  if ((G & 3) == 0) {
+  // rows of both arrays hold a multiple of 16 tokens, so the four are there;
+  // those at or past the length are read and left as they were
+  const float4* z = reinterpret_cast<const float4*>(logits + (bh * stride + t) * G);
+  float x[4 * G];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (4 * i < G) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(z) + i);
-        x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < G) x[i] = __ldcg(z + i);
+  for (int i = 0; i < G; ++i) {
+    const float4 y = __ldcg(z + i);
+    x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
   }
-  float sum = 0.f;
+  float4* wp = reinterpret_cast<float4*>(weights + bh * L_max + t);
+  const float4 old = *wp;
+  float m[G], inv[G];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < G) sum = fmaf(exp2f(x[i] - s_m[i]), s_inv[i], sum);
-  float* w = weights + bh * L_max + t;
-  *w = fresh && t == len_b - 1 ? sum : *w + sum;
+  for (int h = 0; h < G; ++h) {
+    const float2 p = __ldcg(reinterpret_cast<const float2*>(ml) + bh * G + h);
+    m[h] = p.x;
+    inv[h] = 1.f / p.y;
+  }
+  float w[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float sum = 0.f;
+#pragma unroll
+    for (int h = 0; h < G; ++h) sum = fmaf(exp2f(x[i * G + h] - m[h]), inv[h], sum);
+    if (t + i < len_b) w[i] = fresh && t + i == len_b - 1 ? sum : w[i] + sum;
+  }
+  *wp = make_float4(w[0], w[1], w[2], w[3]);
 }
 
-cudaError_t launch_add_weights(const Shape& s, const float* logits, const float* ml,
-                               float* weights, int64_t len, const int32_t* lens, bool fresh,
-                               cudaStream_t st) {
+template <int G>
+static cudaError_t add_weights_t(const Shape& s, const float* logits, const float* ml,
+                                 float* weights, int64_t len, const int32_t* lens, bool fresh,
+                                 cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((len + 255) / 256), s.H, s.B);
+  cfg.gridDim = dim3(static_cast<unsigned>((len + 1023) / 1024), s.H, s.B);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -74,18 +78,34 @@ cudaError_t launch_add_weights(const Shape& s, const float* logits, const float*
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, add_weights_kernel, logits, ml, weights, s.H, s.G,
+  return cudaLaunchKernelEx(&cfg, add_weights_kernel<G>, logits, ml, weights, s.H,
                             (len + kBlock - 1) / kBlock * kBlock, s.L_max, len, lens, fresh);
 }
 
+cudaError_t launch_add_weights(const Shape& s, const float* logits, const float* ml,
+                               float* weights, int64_t len, const int32_t* lens, bool fresh,
+                               cudaStream_t st) {
+  switch (s.G) {
+    case 1: return add_weights_t<1>(s, logits, ml, weights, len, lens, fresh, st);
+    case 2: return add_weights_t<2>(s, logits, ml, weights, len, lens, fresh, st);
+    case 3: return add_weights_t<3>(s, logits, ml, weights, len, lens, fresh, st);
+    case 4: return add_weights_t<4>(s, logits, ml, weights, len, lens, fresh, st);
+    case 5: return add_weights_t<5>(s, logits, ml, weights, len, lens, fresh, st);
+    case 6: return add_weights_t<6>(s, logits, ml, weights, len, lens, fresh, st);
+    case 7: return add_weights_t<7>(s, logits, ml, weights, len, lens, fresh, st);
+    default: return add_weights_t<8>(s, logits, ml, weights, len, lens, fresh, st);
+  }
+}
+
 // ---------------------------------------------------------------------- select
-constexpr int kEvThreads = 512;
-constexpr int kEvCluster = 8;        // CTAs per (row, KV head), each with a slice of its tokens
+constexpr int kEvThreads = 1024;
+constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvCluster = 8;        // CTAs per (row, KV head) of a long row
 
 // order-preserving key of a weight; NaN below every number
 __device__ __forceinline__ uint32_t weight_key(float w) { return w == w ? score_key(w) : 0u; }
 
-// Exclusive prefix sum of x over the CTA's threads; *total receives the sum.
+// Exclusive prefix sum of x over the CTA's threads; total receives the sum.
 __device__ __forceinline__ uint32_t ev_scan(uint32_t x, uint32_t* warp_tot, uint32_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t inc = x;
@@ -96,150 +116,254 @@ __device__ __forceinline__ uint32_t ev_scan(uint32_t x, uint32_t* warp_tot, uint
   }
   if (lane == 31) warp_tot[warp] = inc;
   __syncthreads();
-  uint32_t before = 0, all = 0;
+  uint32_t c = warp_tot[lane], run = c;          // (one total per lane: 32 warps)
 #pragma unroll
-  for (int w = 0; w < kEvThreads / 32; ++w) {
-    const uint32_t c = warp_tot[w];
-    before += w < warp ? c : 0u;
-    all += c;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += y;
   }
+  total = __shfl_sync(0xffffffffu, run, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, run - c, warp);
   __syncthreads();
-  total = all;
   return before + inc - x;
 }
 
-// A cluster of eight CTAs per (row, KV head). Three radix passes (11, 11 and
-// 10 bits of the keys, from the top) find the exact threshold key: every CTA
-// counts its slice into its own histogram, and after a cluster barrier all of
-// them read all eight through distributed shared memory and take the same
-// decision, so one barrier per pass suffices (each pass has a histogram of its
-// own). Then each CTA counts the keys above and equal to the threshold in its
-// slice, the eight counts give its place in the list, and warps that own
-// contiguous ranges write it in order.
+// One CTA (CL = 1) or a cluster of eight per (row, KV head), each CTA with a
+// slice of the candidates in registers: KPT per thread, four consecutive ones
+// per 16-byte load, so that index order is (load u, thread, element). KPT = 0:
+// a slice of any length, read again (from L2) in every pass.
+//
+// Three radix passes (11, 11 and 10 bits of the keys, from the top) find the
+// exact threshold key: every CTA counts its slice into a histogram of its own
+// (one per pass), and after a cluster barrier all of them read all eight
+// through distributed shared memory and take the same decision. A pass after
+// which the threshold bin is taken whole is the last one. Then the keys above
+// and those equal to the threshold are counted per (u, warp); one scan over
+// those counts and the CTAs' totals gives every kept token its place in the
+// list. Latency-bound: a barrier and a round of remote reads per pass.
+template <int CL, int KPT>
 __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* __restrict__ weights,
                                                                   int32_t* __restrict__ kept, int H,
                                                                   int64_t L_max, int64_t len,
                                                                   const int32_t* lens, int budget,
                                                                   int recent, Ctrl* ctrl) {
+  constexpr int U = KPT > 0 ? KPT / 4 : 1;        // loads held per thread
   __shared__ __align__(16) uint32_t hist[3][kBins];
-  __shared__ uint32_t warp_tot[kEvThreads / 32];
-  __shared__ uint32_t s_prefix, s_remaining;
+  __shared__ uint32_t warp_tot[kEvWarps];
+  __shared__ uint32_t tab[U][kEvWarps];           // per (u, warp): keys above | equal << 16
+  __shared__ uint32_t s_prefix, s_remaining, s_whole;
   __shared__ uint32_t s_count[2];                 // keys above, equal to the threshold
   cg::cluster_group cluster = cg::this_cluster();
-  grid_dependency_wait();
+  auto all_sync = [&] {
+    if constexpr (CL > 1) cluster.sync();
+    else __syncthreads();
+  };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = static_cast<int>(cluster.block_rank());
+  const int rank = CL > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+  for (int i = tid; i < 3 * kBins / 4; i += kEvThreads)
+    reinterpret_cast<uint4*>(&hist[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+  grid_dependency_wait();
   const int g = blockIdx.y, b = blockIdx.z;
   const int64_t bh = static_cast<int64_t>(b) * H + g;
   int32_t* out = kept + bh * budget;
   if (rank == 0 && g == 0 && tid == 0 && row_len_bad(lens, len, b)) raise_error(ctrl, kErrBadIndex);
   const int n = static_cast<int>(row_len(lens, len, b));
-  const int all = kEvCluster * kEvThreads;
   const int me = rank * kEvThreads + tid;
   if (n <= budget) {                              // nothing to evict (whole cluster)
-    for (int i = me; i < budget; i += all) out[i] = i < n ? i : -1;
+    for (int i = me; i < budget; i += CL * kEvThreads) out[i] = i < n ? i : -1;
     return;
   }
   const int cand = n - recent, need = budget - recent;
-  for (int i = me; i < recent; i += all) out[need + i] = cand + i;
+  for (int i = me; i < recent; i += CL * kEvThreads) out[need + i] = cand + i;
   if (need == 0) return;
+  // a slice starts at a multiple of 16 tokens, as rows do (16-byte loads)
   const float* w = weights + bh * L_max;
-  const int per = (cand + kEvCluster * 128 - 1) / (kEvCluster * 128) * 128;
+  const int per = (cand + CL * 16 - 1) / (CL * 16) * 16;
   const int c0 = min(cand, rank * per), c1 = min(cand, c0 + per);
-  for (int i = tid; i < 3 * kBins; i += kEvThreads) (&hist[0][0])[i] = 0u;
-  if (tid == 0) { s_prefix = 0u; s_remaining = static_cast<uint32_t>(need); }
-  __syncthreads();
-  // calls f(index, key) for every key of [from, to), four loads at a time
-  auto each = [&](auto&& f) {
-    for (int j0 = c0 + tid * 4; j0 < c1; j0 += 4 * 4 * kEvThreads) {
-      float4 x[4];
+  const int rounds = KPT > 0 ? U : (per + 4 * kEvThreads - 1) / (4 * kEvThreads);
+  uint32_t key[4 * U];
+  uint32_t in = 0;                                // bit 4u + e: key is a candidate
+  auto load = [&](int u, int at) {
+    const int j = c0 + (u * kEvThreads + tid) * 4;
+    const float4 x = j < c1 ? __ldcg(reinterpret_cast<const float4*>(w + j))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j = j0 + u * 4 * kEvThreads;
-        // (a slice starts at a multiple of 128 and rows hold a multiple of 16)
-        if (j < c1) x[u] = __ldcg(reinterpret_cast<const float4*>(w + j));
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j = j0 + u * 4 * kEvThreads;
-        const float y[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + e < c1) f(weight_key(y[e]));
-      }
+    for (int e = 0; e < 4; ++e) {
+      key[at + e] = weight_key(y[e]);
+      if (j + e < c1) in |= 1u << (at + e);
+      else in &= ~(1u << (at + e));
     }
   };
+  if constexpr (KPT > 0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(u, 4 * u);
+  }
+  __syncthreads();                                // the histograms are clear
   uint32_t prefix = 0, remaining = static_cast<uint32_t>(need);
+  int shift = 21;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
     const uint32_t above = pass == 0 ? 0u : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
     uint32_t* h = hist[pass];
-    each([&](uint32_t key) {
-      if ((key & above) == prefix) atomicAdd(&h[(key >> shift) & mask], 1u);
-    });
-    cluster.sync();
-    // thread t owns bins 2047 - 4t .. 2044 - 4t, from the top
-    uint32_t c[4] = {0u, 0u, 0u, 0u};
-    uint4 r[kEvCluster];
+    auto count = [&](int at) {
 #pragma unroll
-    for (int i = 0; i < kEvCluster; ++i)
-      r[i] = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(h, i) + kBins - 4 - 4 * tid);
+      for (int e = 0; e < 4; ++e)
+        if (((in >> (at + e)) & 1u) && (key[at + e] & above) == prefix)
+          atomicAdd(&h[(key[at + e] >> shift) & mask], 1u);
+    };
+    if constexpr (KPT > 0) {
 #pragma unroll
-    for (int i = 0; i < kEvCluster; ++i) {
-      c[0] += r[i].w; c[1] += r[i].z; c[2] += r[i].y; c[3] += r[i].x;
+      for (int u = 0; u < U; ++u) count(4 * u);
+    } else {
+      for (int u = 0; u < rounds; ++u) { load(u, 0); count(0); }
     }
-    uint32_t total;
-    uint32_t before = ev_scan(c[0] + c[1] + c[2] + c[3], warp_tot, total);
+    all_sync();
+    // thread t owns bins 2047 - 2t and 2046 - 2t
+    uint32_t hi = 0, lo = 0;
+    uint2 r[CL];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (before < remaining && remaining <= before + c[e]) {
-        s_prefix = prefix | (static_cast<uint32_t>(kBins - 1 - 4 * tid - e) << shift);
-        s_remaining = remaining - before;
-      }
-      before += c[e];
+    for (int i = 0; i < CL; ++i) {
+      const uint32_t* hr = CL > 1 ? cluster.map_shared_rank(h, i) : h;
+      r[i] = *reinterpret_cast<const uint2*>(hr + kBins - 2 - 2 * tid);
+    }
+#pragma unroll
+    for (int i = 0; i < CL; ++i) { hi += r[i].y; lo += r[i].x; }
+    uint32_t total;
+    const uint32_t before = ev_scan(hi + lo, warp_tot, total);
+    if (before < remaining && remaining <= before + hi + lo) {
+      const bool first = remaining <= before + hi;
+      const uint32_t left = remaining - before - (first ? 0u : hi);
+      s_prefix = prefix | (static_cast<uint32_t>(kBins - 1 - 2 * tid - (first ? 0 : 1)) << shift);
+      s_remaining = left;
+      s_whole = left == (first ? hi : lo);
     }
     __syncthreads();
     prefix = s_prefix;
     remaining = s_remaining;
+    const bool whole = s_whole;
+    if (whole || pass == 2) break;
+    shift = pass == 0 ? 10 : 0;
     __syncthreads();
   }
-  // every key above T, and the `remaining` of lowest index among those equal
-  const uint32_t T = prefix;
-  const int chunk = per / (kEvThreads / 32) > 32 ? (per / (kEvThreads / 32) + 31) / 32 * 32 : 32;
-  const int wb = min(c1, c0 + warp * chunk), we = min(c1, wb + chunk);
-  uint32_t gt = 0, eq = 0;
-  for (int j0 = wb; j0 < we; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t key = j < we ? weight_key(__ldcg(w + j)) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, j < we && key > T));
-    eq += __popc(__ballot_sync(0xffffffffu, j < we && key == T));
-  }
-  uint32_t gt_all, eq_all;
-  uint32_t gt_at = ev_scan(lane == 0 ? gt : 0u, warp_tot, gt_all);
-  uint32_t eq_at = ev_scan(lane == 0 ? eq : 0u, warp_tot, eq_all);
-  gt_at = __shfl_sync(0xffffffffu, gt_at, 0);
-  eq_at = __shfl_sync(0xffffffffu, eq_at, 0);
-  if (tid == 0) { s_count[0] = gt_all; s_count[1] = eq_all; }
-  cluster.sync();
-  for (int i = 0; i < rank; ++i) {
-    const uint32_t* other = cluster.map_shared_rank(s_count, i);
-    gt_at += other[0];
-    eq_at += other[1];
-  }
-  cluster.sync();                                 // no CTA leaves while another reads it
-  uint32_t pos = gt_at + min(eq_at, remaining);
-  const uint32_t lt = (1u << lane) - 1u;
-  for (int j0 = wb; j0 < we; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t key = j < we ? weight_key(__ldcg(w + j)) : 0u;
-    const uint32_t eqb = __ballot_sync(0xffffffffu, j < we && key == T);
-    const bool take = j < we && (key > T || (key == T && eq_at + __popc(eqb & lt) < remaining));
-    eq_at += __popc(eqb);
-    const uint32_t tb = __ballot_sync(0xffffffffu, take);
-    if (take) out[pos + __popc(tb & lt)] = j;
-    pos += __popc(tb);
+  // Kept: every key whose bits above `shift` exceed those of T, and the
+  // `remaining` of lowest index among those with the same bits (all of them
+  // where the bin is taken whole).
+  const uint32_t T = prefix >> shift;
+  auto marks = [&](int at, uint32_t& gt, uint32_t& eq) {
+    gt = 0; eq = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t k = key[at + e] >> shift;
+      if ((in >> (at + e)) & 1u) {
+        gt |= (k > T ? 1u : 0u) << e;
+        eq |= (k == T ? 1u : 0u) << e;
+      }
+    }
+  };
+  // counts of a load over this warp's earlier lanes (exclusive) and in all
+  auto lane_scan = [&](uint32_t gt, uint32_t eq, uint32_t& all) {
+    const uint32_t mine = __popc(gt) | (__popc(eq) << 16);
+    uint32_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    all = __shfl_sync(0xffffffffu, inc, 31);
+    return inc - mine;
+  };
+  uint32_t base_gt = 0, base_eq = 0;              // of this CTA, then running
+  auto place = [&](int u, int at, uint32_t off, uint32_t gt, uint32_t eq) {
+    // off: counts before this thread's four keys, within the CTA
+    uint32_t g_at = base_gt + (off & 0xffffu), e_at = base_eq + (off >> 16);
+    const int j = c0 + (u * kEvThreads + tid) * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if ((gt >> e) & 1u) out[g_at++ + min(e_at, remaining)] = j + e;
+      if ((eq >> e) & 1u) {
+        if (e_at < remaining) out[g_at + e_at] = j + e;
+        ++e_at;
+      }
+    }
+  };
+  if constexpr (KPT > 0) {
+    uint32_t off[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t gt, eq, all;
+      marks(4 * u, gt, eq);
+      off[u] = lane_scan(gt, eq, all);
+      if (lane == 0) tab[u][warp] = all;
+    }
+    __syncthreads();
+    // scan of the table in (u, warp) order, the packed counts of a CTA fit 16 bits
+    if (warp == 0) {
+      uint32_t run = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t c = tab[u][lane];
+        uint32_t inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        tab[u][lane] = run + inc - c;
+        run += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      if (lane == 0) { s_count[0] = run & 0xffffu; s_count[1] = run >> 16; }
+    }
+    if constexpr (CL > 1) {
+      cluster.sync();
+      for (int i = 0; i < rank; ++i) {
+        const uint32_t* other = cluster.map_shared_rank(s_count, i);
+        base_gt += other[0];
+        base_eq += other[1];
+      }
+      cluster.sync();                             // no CTA leaves while another reads it
+    } else {
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t gt, eq;
+      marks(4 * u, gt, eq);
+      place(u, 4 * u, tab[u][warp] + off[u], gt, eq);
+    }
+  } else {
+    // the CTA's totals first, then round by round
+    uint32_t n_gt = 0, n_eq = 0;
+    for (int u = 0; u < rounds; ++u) {
+      uint32_t gt, eq;
+      load(u, 0);
+      marks(0, gt, eq);
+      n_gt += __popc(gt);
+      n_eq += __popc(eq);
+    }
+    uint32_t t_gt, t_eq;
+    (void)ev_scan(n_gt, warp_tot, t_gt);
+    (void)ev_scan(n_eq, warp_tot, t_eq);
+    if (tid == 0) { s_count[0] = t_gt; s_count[1] = t_eq; }
+    all_sync();
+    if constexpr (CL > 1) {
+      for (int i = 0; i < rank; ++i) {
+        const uint32_t* other = cluster.map_shared_rank(s_count, i);
+        base_gt += other[0];
+        base_eq += other[1];
+      }
+      cluster.sync();
+    }
+    for (int u = 0; u < rounds; ++u) {
+      uint32_t gt, eq, all;
+      load(u, 0);
+      marks(0, gt, eq);
+      const uint32_t off = ev_scan(__popc(gt) | (__popc(eq) << 16), warp_tot, all);
+      place(u, 0, off, gt, eq);
+      base_gt += all & 0xffffu;
+      base_eq += all >> 16;
+    }
   }
 }
 
@@ -330,22 +454,34 @@ static cudaError_t gather_t(const Shape& s, const EvictArgs& a, cudaStream_t st)
   return cudaLaunchKernelEx(&cfg, evict_gather_kernel<T, D>, a, s.H, s.L_max, M, total);
 }
 
-cudaError_t launch_evict(const Shape& s, const EvictArgs& a, cudaStream_t st) {
+template <int CL, int KPT>
+static cudaError_t evict_select_t(const Shape& s, const EvictArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kEvCluster, s.H, s.B);
+  cfg.gridDim = dim3(CL, s.H, s.B);
   cfg.blockDim = dim3(kEvThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kEvCluster;
+  attr[0].val.clusterDim.x = CL;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a.weights, a.kept, s.H, s.L_max,
-                                     a.len, a.lens, a.budget, a.recent, a.ctrl);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<CL, KPT>, a.weights, a.kept, s.H, s.L_max,
+                            a.len, a.lens, a.budget, a.recent, a.ctrl);
+}
+
+// One CTA up to 8192 tokens (no cluster barriers), eight up to 131072 with
+// their slices in registers, eight of any length beyond (32 keys per thread
+// spill).
+cudaError_t launch_evict(const Shape& s, const EvictArgs& a, cudaStream_t st) {
+  cudaError_t e;
+  if (a.len <= 8 * kEvThreads) e = evict_select_t<1, 8>(s, a, st);
+  else if (a.len <= 8 * kEvCluster * kEvThreads) e = evict_select_t<kEvCluster, 8>(s, a, st);
+  else if (a.len <= 16 * kEvCluster * kEvThreads) e = evict_select_t<kEvCluster, 16>(s, a, st);
+  else e = evict_select_t<kEvCluster, 0>(s, a, st);
   if (e != cudaSuccess) return e;
   if (s.bf16)
     return s.D == 128 ? gather_t<__nv_bfloat16, 128>(s, a, st) : gather_t<__nv_bfloat16, 64>(s, a, st);

@@ -62,38 +62,71 @@ __device__ __forceinline__ void load8<float>(const float* p, float (&f)[8]) {
   Chunk<float>::unpack(b, f + 4);
 }
 
-// Scale, zero (as their bf16 values) and the eight codes (nibble i = channel i)
-// of this lane's 8 channels; the group's 8 lanes are lane & ~7 .. lane | 7 and
-// all of them call this together.
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Eight codes (nibble i = channel i) of x for a group's scale and zero:
+// rint(fl((x - zero) / scale)), with inv = fl(1 / scale).
 //
-// code = rint(fl((x - zero) / scale)) needs the correctly rounded quotient
-// only next to a half: the product with the reciprocal is within 15 * 2^-22 of
-// it, so unless some product lies within 2^-16 of a half its rounding is the
-// quotient's, and the eight divisions (about ten instructions each, more than
-// the copy's bandwidth leaves per element) are done only then.
-__device__ __forceinline__ uint32_t kv4_encode8(const float (&x)[8], float& scale, float& zero) {
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) { lo = fminf(lo, x[i]); hi = fmaxf(hi, x[i]); }
-#pragma unroll
-  for (int m = 1; m < 8; m <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-  }
-  zero = __bfloat162float(__float2bfloat16_rn(lo));
-  scale = __bfloat162float(__float2bfloat16_rn(__fmul_rn(__fsub_rn(hi, lo), kKv4Inv15)));
+// The rounded quotient comes without a division. With d = fl(x - zero) and
+// q0 = fl(d inv), which is within 2^-22 of d / scale relatively, the residual
+// d - q0 scale is exact in one fused operation (scale has 8 significant bits,
+// so q0 scale has 32, of which the upper 22 cancel), and q0 + residual inv is
+// within 2^-45 of the quotient before its one rounding. A quotient of a 24-bit
+// by an 8-bit number that is not itself half-way between two fp32 numbers is
+// at least 2^-34 away from there, so that rounding is the quotient's. This
+// needs inv and the residual to be normal numbers: scales below 1e-30 take
+// the division (a constant group's scale is 0, its codes are 0).
+//
+// EXACT_ZERO: x holds bf16 values, whose minimum the zero is; then no quotient
+// leaves [0, 15.5) and nothing is clamped.
+template <bool EXACT_ZERO>
+__device__ __forceinline__ uint32_t kv4_codes8(const float (&x)[8], float scale, float zero,
+                                               float inv) {
   constexpr float kMagic = 12582912.f;           // 1.5 * 2^23: adding it rounds to an integer
-  const float inv = __frcp_rn(scale);
-  float worst = 0.f;
-  uint32_t w = 0;
+  const uint64_t nz = f2_pack(-zero, -zero), iv = f2_pack(inv, inv);
+  const uint64_t ns = f2_pack(-scale, -scale);
+  const uint64_t up = f2_pack(kMagic, kMagic), down = f2_pack(-kMagic, -kMagic);
+  float c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = fminf(fmaxf((x[i] - zero) * inv, 0.f), 15.f);
-    const float r = q + kMagic;
-    worst = fmaxf(worst, fabsf(q - (r - kMagic)));
-    w |= (__float_as_uint(r) & 15u) << (4 * i);
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t d = f2_add(f2_pack(x[2 * i], x[2 * i + 1]), nz);
+    const uint64_t q0 = f2_mul(d, iv);
+    uint64_t q = f2_fma(f2_fma(q0, ns, d), iv, q0);
+    if constexpr (!EXACT_ZERO) {
+      float a, b;
+      f2_unpack(q, a, b);
+      q = f2_pack(fminf(fmaxf(a, 0.f), 15.f), fminf(fmaxf(b, 0.f), 15.f));
+    }
+    f2_unpack(f2_add(f2_add(q, up), down), c[2 * i], c[2 * i + 1]);
   }
-  if (!(worst < 0.5f - 1.0f / 65536.f) || !(scale > 1e-30f)) {
+  // four codes at a time as one number below 2^16, exact in fp32
+  const float lo = fmaf(fmaf(fmaf(c[3], 16.f, c[2]), 16.f, c[1]), 16.f, c[0]);
+  const float hi = fmaf(fmaf(fmaf(c[7], 16.f, c[6]), 16.f, c[5]), 16.f, c[4]);
+  uint32_t w = __byte_perm(__float_as_uint(lo + 8388608.f), __float_as_uint(hi + 8388608.f), 0x5410);
+  if (!(scale > 1e-30f)) {
     w = 0;
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {
@@ -106,6 +139,75 @@ __device__ __forceinline__ uint32_t kv4_encode8(const float (&x)[8], float& scal
     }
   }
   return w;
+}
+
+__device__ __forceinline__ void kv4_scale_zero(float lo, float hi, float& scale, float& zero) {
+  zero = __bfloat162float(__float2bfloat16_rn(lo));
+  scale = __bfloat162float(__float2bfloat16_rn(__fmul_rn(__fsub_rn(hi, lo), kKv4Inv15)));
+}
+
+// Scale, zero and codes of this lane's 8 channels; the group's 8 lanes are
+// lane & ~7 .. lane | 7 and all of them call this together.
+__device__ __forceinline__ uint32_t kv4_encode8(const float (&x)[8], float& scale, float& zero) {
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) { lo = fminf(lo, x[i]); hi = fmaxf(hi, x[i]); }
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+  }
+  kv4_scale_zero(lo, hi, scale, zero);
+  return kv4_codes8<false>(x, scale, zero, __frcp_rn(scale));
+}
+// The same for eight bf16 values as they lie in memory (minima and maxima two
+// at a time).
+__device__ __forceinline__ uint32_t kv4_encode8(const uint4& raw, float& scale, float& zero) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  auto mn = [](uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                     *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  };
+  auto mx = [](uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                     *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  };
+  uint32_t lo = mn(mn(w[0], w[1]), mn(w[2], w[3])), hi = mx(mx(w[0], w[1]), mx(w[2], w[3]));
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) {
+    lo = mn(lo, __shfl_xor_sync(0xffffffffu, lo, m));
+    hi = mx(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+  }
+  kv4_scale_zero(fminf(bf16_lo(lo), bf16_hi(lo)), fmaxf(bf16_lo(hi), bf16_hi(hi)), scale, zero);
+  float x[8];
+  Chunk<__nv_bfloat16>::unpack(raw, x);
+  return kv4_codes8<true>(x, scale, zero, __frcp_rn(scale));
+}
+
+// Transpose of an 8 x 8 matrix of nibbles: nibble c of word r <-> nibble r of
+// word c.
+__device__ __forceinline__ void nibble_transpose(uint32_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {                  // 4 x 4 halves
+    const uint32_t a = w[i], b = w[i + 4];
+    w[i] = __byte_perm(a, b, 0x5410);
+    w[i + 4] = __byte_perm(a, b, 0x7632);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (i & 2) continue;                         // 2 x 2 bytes
+    const uint32_t a = w[i], b = w[i + 2];
+    w[i] = __byte_perm(a, b, 0x6240);
+    w[i + 2] = __byte_perm(a, b, 0x7351);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {               // nibbles of a byte
+    const uint32_t a = w[i], b = w[i + 1];
+    w[i] = (a & 0x0f0f0f0fu) | ((b & 0x0f0f0f0fu) << 4);
+    w[i + 1] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+  }
 }
 
 // bf16 {scale, zero} of one tensor as the record holds them

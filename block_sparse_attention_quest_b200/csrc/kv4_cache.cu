@@ -7,9 +7,34 @@ namespace resa {
 // Rows to records. One warp per (record, K or V): a lane owns 8 channels of a
 // token, the 8 lanes of a 64-channel group find its minimum and maximum with
 // three shuffles each. The key words of a lane's 8 channels are whole words of
-// the record; the value words mix four tokens and two channels, so the value
-// codes pass through shared memory. Tokens past the row's length count as
-// zeros (code 0, scale 0, zero 0).
+// the record; the value words mix four tokens and two times eight channels,
+// one 8 x 8 transpose of nibbles for each (group, token pair, 16 channels),
+// done by one lane on words taken from shared memory. Tokens past the row's
+// length count as zeros (code 0, scale 0, zero 0).
+//
+// Bound by HBM (4 B read and 1.1 B written per element pair) if an element
+// costs less than about 14 instructions; see kv4_codes8 for what that takes.
+template <typename T> struct Kv4Raw;
+template <> struct Kv4Raw<__nv_bfloat16> {
+  uint4 x;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = ld_stream16(p); }
+  __device__ __forceinline__ void clear() { x = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ uint32_t encode(float& scale, float& zero) const {
+    return kv4_encode8(x, scale, zero);
+  }
+};
+template <> struct Kv4Raw<float> {
+  float x[8];
+  __device__ __forceinline__ void load(const float* p) { load8<float>(p, x); }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+  }
+  __device__ __forceinline__ uint32_t encode(float& scale, float& zero) const {
+    return kv4_encode8(x, scale, zero);
+  }
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_quantize_kernel(const T* __restrict__ k,
                                                            const T* __restrict__ v,
@@ -23,7 +48,7 @@ __global__ void __launch_bounds__(256) kv4_quantize_kernel(const T* __restrict__
   constexpr int PASSES = kBlock / TPP;
   constexpr int REC = kv4_record_bytes(D);
   __shared__ __align__(16) uint8_t stage[4][REC];   // one record per pair of warps
-  __shared__ __align__(16) uint32_t vcode[4][kBlock][D / 8];
+  __shared__ __align__(16) uint32_t vcode[4][kBlock][D / 8 + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pair = warp >> 1;
   const bool is_v = warp & 1;
@@ -41,22 +66,18 @@ __global__ void __launch_bounds__(256) kv4_quantize_kernel(const T* __restrict__
   uint8_t* rec = stage[pair];
   if (live) {
     const T* src = (is_v ? v : k) + (bh * L_max + t0) * D + chunk * 8;
-    float x[PASSES][8];
+    Kv4Raw<T> x[PASSES];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       const int t = r0 + p * TPP;
-      if (t < valid) {
-        load8<T>(src + static_cast<int64_t>(t) * D, x[p]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[p][e] = 0.f;
-      }
+      if (t < valid) x[p].load(src + static_cast<int64_t>(t) * D);
+      else x[p].clear();
     }
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       const int t = r0 + p * TPP;
       float scale, zero;
-      const uint32_t w = kv4_encode8(x[p], scale, zero);
+      const uint32_t w = x[p].encode(scale, zero);
       if (is_v) {
         vcode[pair][t][chunk] = w;
       } else {
@@ -70,28 +91,24 @@ __global__ void __launch_bounds__(256) kv4_quantize_kernel(const T* __restrict__
     }
     if (is_v) {
       __syncwarp();
-      // lane (r, c): word m of group g holds tokens 2c, 2c + 1, 2c + 8, 2c + 9
-      // of channels 16m + r and 16m + 8 + r
-      const int r = lane >> 2, c = lane & 3;
+      // lane (g, c, m): nibble e + 2h + 4o of the words r = 0 .. 7 is token
+      // 8h + 2c + o, channel 16m + 8e + r
+      const int gg = lane >> 4, c = (lane >> 2) & 3, m = lane & 3;
+      if (gg < NG) {
+        uint32_t w[8];
 #pragma unroll
-      for (int gg = 0; gg < NG; ++gg) {
-        uint32_t out[4];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          uint32_t w = 0;
+          for (int o = 0; o < 2; ++o) {
+            const uint2 cd = *reinterpret_cast<const uint2*>(
+                &vcode[pair][8 * h + 2 * c + o][gg * 8 + 2 * m]);
+            w[2 * h + 4 * o] = cd.x;
+            w[1 + 2 * h + 4 * o] = cd.y;
+          }
+        nibble_transpose(w);
+        uint8_t* dst = rec + kv4_value_word_at(D, 2 * c, gg, m);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const uint2 cd = *reinterpret_cast<const uint2*>(
-                  &vcode[pair][8 * h + 2 * c + o][gg * 8 + 2 * m]);
-              w |= ((cd.x >> (4 * r)) & 15u) << (4 * (2 * h + 4 * o));
-              w |= ((cd.y >> (4 * r)) & 15u) << (4 * (1 + 2 * h + 4 * o));
-            }
-          out[m] = w;
-        }
-        *reinterpret_cast<uint4*>(rec + kv4_code_bytes(D) + gg * 512 + lane * 16) =
-            make_uint4(out[0], out[1], out[2], out[3]);
+        for (int r = 0; r < 8; ++r) *reinterpret_cast<uint32_t*>(dst + r * 64) = w[r];
       }
     }
   }
@@ -103,8 +120,47 @@ __global__ void __launch_bounds__(256) kv4_quantize_kernel(const T* __restrict__
   }
 }
 
-// Records to rows: one warp per record; zero + scale * code in fp32 (the
-// product is exact), rounded once to the cache type.
+// Eight values zero + scale * code of a word's nibbles, in fp32 (the product
+// is exact; a code becomes a float as the low bits of 2^23 + code).
+__device__ __forceinline__ void kv4_decode8(uint32_t w, uint32_t meta, float (&f)[8]) {
+  const float s = bf16_lo(meta), z = bf16_hi(meta);
+  const uint64_t s2 = f2_pack(s, s), z2 = f2_pack(z, z), down = f2_pack(-8388608.f, -8388608.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = __uint_as_float(((w >> (8 * i)) & 15u) | 0x4b000000u);
+    const float b = __uint_as_float(((w >> (8 * i + 4)) & 15u) | 0x4b000000u);
+    f2_unpack(f2_fma(f2_add(f2_pack(a, b), down), s2, z2), f[2 * i], f[2 * i + 1]);
+  }
+}
+
+// 16 consecutive channels of a token
+__device__ __forceinline__ void store16(float* p, bool, const float (&a)[8], const float (&b)[8]) {
+  float4* q = reinterpret_cast<float4*>(p);
+  q[0] = make_float4(a[0], a[1], a[2], a[3]);
+  q[1] = make_float4(a[4], a[5], a[6], a[7]);
+  q[2] = make_float4(b[0], b[1], b[2], b[3]);
+  q[3] = make_float4(b[4], b[5], b[6], b[7]);
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, bool wide, const float (&a)[8],
+                                        const float (&b)[8]) {
+  const uint4 x = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                             pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+  const uint4 y = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]),
+                             pack_bf16x2(b[4], b[5]), pack_bf16x2(b[6], b[7]));
+  if (wide) {                                     // a whole sector from one lane
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"l"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(y.x), "r"(y.y), "r"(y.z),
+                   "r"(y.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = x;
+    reinterpret_cast<uint4*>(p)[1] = y;
+  }
+}
+
+// Records to rows, rounded once to the cache type. One warp per (record, K or
+// V); lane (g, c, m) has the sixteen channels 64g + 16m .. + 15 of four
+// tokens, for values the four of an inverse transpose of nibbles.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_dequantize_kernel(const uint8_t* __restrict__ kv4,
                                                              T* __restrict__ k, T* __restrict__ v,
@@ -112,11 +168,10 @@ __global__ void __launch_bounds__(256) kv4_dequantize_kernel(const uint8_t* __re
                                                              int64_t len, int64_t total,
                                                              const int32_t* lens, int H) {
   constexpr int REC = kv4_record_bytes(D);
-  constexpr int LPR = D / 8;
-  constexpr int TPP = 32 / LPR;
-  __shared__ __align__(16) uint8_t stage[8][REC];
+  constexpr int NG = D / kKv4Group;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  const bool is_v = warp & 1;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + (warp >> 1);
   if (id >= total) return;
   const int64_t bh = id / M;
   const int j = static_cast<int>(id % M);
@@ -124,40 +179,51 @@ __global__ void __launch_bounds__(256) kv4_dequantize_kernel(const uint8_t* __re
   const int64_t t0 = static_cast<int64_t>(j) * kBlock;
   if (t0 >= len_b) return;
   const int valid = static_cast<int>(len_b - t0 < kBlock ? len_b - t0 : kBlock);
-  const uint8_t* src = kv4 + (bh * Mmax + j) * REC;
-  uint8_t* rec = stage[warp];
-  for (int i = lane; i < REC / 16; i += 32)
-    *reinterpret_cast<uint4*>(rec + i * 16) = ld_stream16(src + i * 16);
-  __syncwarp();
-  const int chunk = lane % LPR, r0 = lane / LPR;
-  const int g = chunk / 8, x8 = chunk % 8;
-  auto store = [&](T* dst, const float (&f)[8]) {
-    if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
-      *reinterpret_cast<float4*>(dst + 4) = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-      *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                  pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-    }
-  };
-#pragma unroll 2
-  for (int t = r0; t < valid; t += TPP) {
-    const uint2 meta = *reinterpret_cast<const uint2*>(rec + kv4_meta_at(D, t, g));
-    const uint32_t kw = *reinterpret_cast<const uint32_t*>(
-        rec + g * 512 + ((t & 7) * 4 + (x8 >> 1)) * 16 + ((t >> 3) * 2 + (x8 & 1)) * 4);
-    const int m = x8 >> 1, e = x8 & 1;
-    const int sh = 4 * (e + 2 * (t >> 3) + 4 * (t & 1));
-    float fk[8], fv[8];
+  const int g = lane >> 4, c = (lane >> 2) & 3, m = lane & 3;
+  if (g >= NG) return;
+  // (the caches are 16-byte aligned; 32-byte stores need twice that)
+  const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31) == 0;
+  const uint8_t* rec = kv4 + (bh * Mmax + j) * REC;
+  T* dst = (is_v ? v : k) + (bh * L_max + t0) * D + g * 64 + m * 16;
+  if (is_v) {
+    uint32_t w[8];
+    const uint8_t* src = rec + kv4_value_word_at(D, 2 * c, g, m);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t vw =
-          *reinterpret_cast<const uint32_t*>(rec + kv4_value_word_at(D, t, g, m) + i * 64);
-      fk[i] = fmaf(bf16_lo(meta.x), static_cast<float>((kw >> (4 * i)) & 15u), bf16_hi(meta.x));
-      fv[i] = fmaf(bf16_lo(meta.y), static_cast<float>((vw >> sh) & 15u), bf16_hi(meta.y));
+    for (int r = 0; r < 8; ++r) w[r] = __ldg(reinterpret_cast<const uint32_t*>(src + r * 64));
+    uint32_t meta[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)                   // token 8 (i / 2) + 2c + i % 2
+      meta[i] = __ldg(reinterpret_cast<const uint32_t*>(
+          rec + kv4_meta_at(D, 8 * (i >> 1) + 2 * c + (i & 1), g) + 4));
+    nibble_transpose(w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 8 * (i >> 1) + 2 * c + (i & 1);
+      if (t >= valid) continue;
+      float a[8], b[8];
+      kv4_decode8(w[2 * (i >> 1) + 4 * (i & 1)], meta[i], a);
+      kv4_decode8(w[1 + 2 * (i >> 1) + 4 * (i & 1)], meta[i], b);
+      store16(dst + static_cast<int64_t>(t) * D, wide, a, b);
     }
-    const int64_t at = (bh * L_max + t0 + t) * D + chunk * 8;
-    store(k + at, fk);
-    store(v + at, fv);
+  } else {
+    // words [r][m][2h], [r][m][2h + 1] of token 8h + r; lane's tokens c, c + 4, ...
+    uint2 w[4];
+    uint32_t meta[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = c + 4 * i;
+      w[i] = __ldg(reinterpret_cast<const uint2*>(rec + g * 512 + ((t & 7) * 4 + m) * 16 + (t >> 3) * 8));
+      meta[i] = __ldg(reinterpret_cast<const uint32_t*>(rec + kv4_meta_at(D, t, g)));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = c + 4 * i;
+      if (t >= valid) continue;
+      float a[8], b[8];
+      kv4_decode8(w[i].x, meta[i], a);
+      kv4_decode8(w[i].y, meta[i], b);
+      store16(dst + static_cast<int64_t>(t) * D, wide, a, b);
+    }
   }
 }
 
@@ -261,7 +327,7 @@ static cudaError_t dequantize_t(const Shape& s, const void* kv4, void* k, void* 
                                 const int32_t* lens, cudaStream_t st) {
   const int M = static_cast<int>((len + kBlock - 1) / kBlock);
   const int64_t total = static_cast<int64_t>(s.B) * s.H * M;
-  kv4_dequantize_kernel<T, D><<<static_cast<unsigned>((total + 7) / 8), 256, 0, st>>>(
+  kv4_dequantize_kernel<T, D><<<static_cast<unsigned>((total + 3) / 4), 256, 0, st>>>(
       static_cast<const uint8_t*>(kv4), static_cast<T*>(k), static_cast<T*>(v), s.L_max, s.Mmax, M,
       len, total, lens, s.H);
   return cudaGetLastError();

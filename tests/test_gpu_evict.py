@@ -174,6 +174,16 @@ def test_evict_budget_above_every_length(resa):
     run_evict(resa, k, v, weights_of("heavy", 1, 2, 64), [50], 100, 10, "bf16", 112)
 
 
+@pytest.mark.parametrize("n", [8192, 8193, 65537, 131072])
+def test_evict_at_the_kernels_bounds(resa, n):
+    """Lengths at which the selection changes its number of CTAs or of keys per
+    thread."""
+    cap = (n + 15) // 16 * 16
+    k, v = rnd(1, 1, 1, cap, 64), rnd(2, 1, 1, cap, 64)
+    for kind in ("heavy", "equal", "few", "odd"):
+        run_evict(resa, k, v, weights_of(kind, 1, 1, cap), [n], n // 3, 17, "bf16", (n // 3 + 15) // 16 * 16)
+
+
 def test_evict_long_row(resa):
     n = 262144 + 333
     cap = (n + 15) // 16 * 16

@@ -87,6 +87,21 @@ def test_quantize_bytes_and_values(resa, dtype, d, lens):
             assert (x[b, :, n:] == 3.0).all()
 
 
+def test_caches_that_are_only_16_byte_aligned(resa):
+    k, v = kv_inputs(3, 1, 2, 48, 64, "bf16")
+    rec = torch.zeros(1, 2, 3, ops.kv4_record_bytes(64), dtype=torch.uint8, device="cuda")
+    buf = torch.zeros(4, k.size + 8, dtype=torch.bfloat16, device="cuda")
+    kt, vt, kb, vb = (b[8:8 + k.size].view(k.shape) for b in buf)
+    kt.copy_(dev(k, "bf16")), vt.copy_(dev(v, "bf16"))
+    assert kt.data_ptr() % 32 == 16 or vt.data_ptr() % 32 == 16
+    resa.kv4_quantize(kt, vt, 48, rec, 2)
+    resa.kv4_dequantize(rec, 48, kb, vb, 2)
+    for got, (c, s, z) in zip((kb, vb), ops.kv4_unpack(rec.cpu().numpy(), 64)):
+        want = ops.bf16_round(ops.kv4_value(c, s, z).astype(np.float32))
+        assert np.array_equal(got.float().cpu().numpy(), want)
+    assert np.array_equal(rec.cpu().numpy(), ops.kv4_pack(k, v, [48]))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_appended_tokens_equal_a_whole_quantisation(resa, dtype, d):
