@@ -20,8 +20,8 @@ namespace resa {
 namespace cg = cooperative_groups;
 
 // Grid (tokens / 1024, H, B), 256 threads; a thread adds the weights of four
-// consecutive tokens, whose logits (four times G values) and sums it requests
-// together.
+// tokens 256 apart, so that every load of a warp is one contiguous run, and
+// requests all of its logits and sums before it uses any.
 template <int G>
 __global__ void __launch_bounds__(256) add_weights_kernel(const float* __restrict__ logits,
                                                           const float* __restrict__ ml,
@@ -34,19 +34,26 @@ __global__ void __launch_bounds__(256) add_weights_kernel(const float* __restric
   const int g = blockIdx.y, b = blockIdx.z;
   const int64_t bh = static_cast<int64_t>(b) * H + g;
   const int64_t len_b = row_len(lens, len, b);
-  const int64_t t = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (t >= len_b) return;
-  // rows of both arrays hold a multiple of 16 tokens, so the four are there;
-  // those at or past the length are read and left as they were
-  const float4* z = reinterpret_cast<const float4*>(logits + (bh * stride + t) * G);
-  float x[4 * G];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x;
+  const float* z = logits + (bh * stride + t0) * G;
+  float* wp = weights + bh * L_max + t0;
+  float x[4][G], old[4];
 #pragma unroll
-  for (int i = 0; i < G; ++i) {
-    const float4 y = __ldcg(z + i);
-    x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
+  for (int i = 0; i < 4; ++i) {
+    if (t0 + i * 256 >= len_b) continue;
+    const float* zi = z + static_cast<int64_t>(i) * 256 * G;
+    if constexpr (G % 4 == 0) {
+#pragma unroll
+      for (int h = 0; h < G; h += 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(zi + h));
+        x[i][h] = y.x; x[i][h + 1] = y.y; x[i][h + 2] = y.z; x[i][h + 3] = y.w;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < G; ++h) x[i][h] = __ldcg(zi + h);
+    }
+    old[i] = wp[i * 256];
   }
-  float4* wp = reinterpret_cast<float4*>(weights + bh * L_max + t);
-  const float4 old = *wp;
   float m[G], inv[G];
 #pragma unroll
   for (int h = 0; h < G; ++h) {
@@ -54,15 +61,15 @@ __global__ void __launch_bounds__(256) add_weights_kernel(const float* __restric
     m[h] = p.x;
     inv[h] = 1.f / p.y;
   }
-  float w[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    const int64_t t = t0 + i * 256;
+    if (t >= len_b) continue;
     float sum = 0.f;
 #pragma unroll
-    for (int h = 0; h < G; ++h) sum = fmaf(exp2f(x[i * G + h] - m[h]), inv[h], sum);
-    if (t + i < len_b) w[i] = fresh && t + i == len_b - 1 ? sum : w[i] + sum;
+    for (int h = 0; h < G; ++h) sum = fmaf(exp2f(x[i][h] - m[h]), inv[h], sum);
+    wp[i * 256] = fresh && t == len_b - 1 ? sum : old[i] + sum;
   }
-  *wp = make_float4(w[0], w[1], w[2], w[3]);
 }
 
 template <int G>
@@ -162,6 +169,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* _
   const int rank = CL > 1 ? static_cast<int>(cluster.block_rank()) : 0;
   for (int i = tid; i < 3 * kBins / 4; i += kEvThreads)
     reinterpret_cast<uint4*>(&hist[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+  grid_launch_dependents();                       // the gather waits for this grid's end
   grid_dependency_wait();
   const int g = blockIdx.y, b = blockIdx.z;
   const int64_t bh = static_cast<int64_t>(b) * H + g;
