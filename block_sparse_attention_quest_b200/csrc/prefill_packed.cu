@@ -64,14 +64,20 @@ struct PackedCfg {
   static constexpr int kNeed = (2 + kSlots) * kTileBytes + 1024;
   static constexpr int kSmem = kNeed > 116 * 1024 ? kNeed : 116 * 1024;
   // twelve warps start with 168 registers each; the softmax warps, which hold
-  // a row of S, take 208, the third warpgroup leaves them (2 * 208 + 88 = 3 * 168)
+  // a row of S, take 200, the third warpgroup leaves them (2 * 200 + 104 = 3 * 168)
   static constexpr int kThreads = 12 * 32;
-  static constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+  static constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 };
 
 __device__ __forceinline__ float ex2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 
@@ -156,8 +162,8 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
                           const __grid_constant__ CUtensorMap tmV, PackedK a) {
   using C = PackedCfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_q[2], bar_full[C::kSlots], bar_empty[C::kSlots];
-  __shared__ __align__(8) uint64_t bar_s[2], bar_p[2], bar_o[2];
+  __shared__ __align__(8) uint64_t bar_q[2], bar_full[C::kSlots], bar_free[3];
+  __shared__ __align__(8) uint64_t bar_s[2], bar_p[2][2], bar_o[2];   // [tile], P: [tile][half of the keys]
   __shared__ uint32_t tmem_base_sh;
   __shared__ int s_seq, s_block;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -219,14 +225,16 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bar_q[w], 1);
       mbar_init(&bar_s[w], 1);
-      mbar_init(&bar_p[w], 128);
+      mbar_init(&bar_p[w][0], 128);
+      mbar_init(&bar_p[w][1], 128);
       mbar_init(&bar_o[w], 1);
     }
 #pragma unroll
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&bar_full[i], 1);
-      mbar_init(&bar_empty[i], 1);
     }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) mbar_init(&bar_free[i], 1);
     fence_mbar_init();
   }
   if (warp == 8) tc::alloc(&tmem_base_sh, 512);
@@ -257,9 +265,12 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
       bool ok = true;
       for (; n < 2 * n_tiles; ++n) {
         const int i = n % C::kSlots;
-        if (n >= C::kSlots &&
-            !(ok = mbar_wait_bounded(&bar_empty[i], (n / C::kSlots - 1) & 1, a.ctrl)))
-          break;
+        if (n >= C::kSlots && (n == C::kSlots || (n - C::kSlots) % 2 == 1)) {
+          // the slot's last tile, copy n - 5, is given back with the one
+          // before or after it: K 0 alone first, then V t and K t + 1 together
+          const int f = (n - C::kSlots + 1) / 2;
+          if (!(ok = mbar_wait_bounded(&bar_free[f % 3], (f / 3) & 1, a.ctrl))) break;
+        }
         mbar_arrive_expect_tx(&bar_full[i], C::kTileBytes);
         const CUtensorMap* map = n & 1 ? &tmV : &tmK;
 #pragma unroll
@@ -280,52 +291,71 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idS = tc::idesc_bf16(128, 128, false);
       constexpr uint32_t idO = tc::idesc_bf16(128, D, true);
-      auto qk = [&](int w, int t) {
-        const uint32_t qa = smem_u32(sQ(w)), ka = smem_u32(slot(2 * t));
+      constexpr uint32_t hi = tc::desc_hi(1024);
+      constexpr uint32_t kTileLo = C::kTileBytes >> 4, kHalfLo = C::kHalfBytes >> 4;
+      const uint32_t q_lo = tc::desc_lo(smem_u32(sQ(0)), 16);
+      const uint32_t k_lo = tc::desc_lo(smem_u32(slot(0)), 16);
+      const uint32_t v_lo = tc::desc_lo(smem_u32(slot(0)), C::kHalfBytes);
+      // the ring slot in use and its phase; slots are taken in the order they
+      // are filled: K 0, V 0, K 1, V 1, ...
+      auto qk = [&](int w, uint32_t i) {
+        const uint32_t ql = q_lo + w * kTileLo, kl = k_lo + i * kTileLo, d = tS(w);
+        tc::mma_ss_lo<false>(d, ql, kl, hi, idS);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::kHalfBytes + (kk & 3) * 32;
-          tc::mma_ss(tS(w), tc::smem_desc(qa + off, 16, 1024), tc::smem_desc(ka + off, 16, 1024),
-                     idS, kk > 0);
+        for (int kk = 1; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalfLo + (kk & 3) * 2;
+          tc::mma_ss_lo<true>(d, ql + off, kl + off, hi, idS);
         }
         tc::commit(&bar_s[w]);
       };
-      auto pv = [&](int w, int t) {
-        const uint32_t va = smem_u32(slot(2 * t + 1));
+      auto pv = [&](int w, int half, uint32_t i, uint32_t acc) {   // 64 keys
+        const uint32_t vl = v_lo + i * kTileLo + half * 512, d = tO(w), p = tS(w) + 32u * half;
+        tc::mma_ts_lo(d, p, vl, hi, idO, acc);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_ts(tO(w), tS(w) + 8u * kk, tc::smem_desc(va + kk * 2048, C::kHalfBytes, 1024), idO,
-                     t > 0 || kk > 0);
+        for (int kk = 1; kk < 4; ++kk) tc::mma_ts_lo(d, p + 8u * kk, vl + kk * 128, hi, idO, 1u);
       };
-      auto full = [&](int n) {
-        return mbar_wait_bounded(&bar_full[n % C::kSlots], (n / C::kSlots) & 1, a.ctrl);
-      };
-      bool ok = full(0);
+      bool ok = mbar_wait_bounded(&bar_full[0], 0, a.ctrl);
       for (int w = 0; ok && w < (nt_b > 0 ? 2 : 1); ++w) {
         if (!(ok = mbar_wait_bounded(&bar_q[w], 0, a.ctrl))) break;
         tc::fence_after_sync();
         qk(w, 0);
       }
-      if (ok) tc::commit(&bar_empty[0]);
+      if (ok) tc::commit(&bar_free[0]);
+      uint32_t f = 1;                              // give-back t + 1 on barrier f
+      uint32_t i = 1, ph = 0;                      // slot and phase of V of tile t
       for (int t = 0; ok && t < n_tiles; ++t) {
-        if (!(ok = full(2 * t + 1))) break;
-        for (int w = 0; ok && w < 2; ++w) {
+        uint32_t i2 = i + 1, ph2 = ph;             // of K of tile t + 1
+        if (i2 == C::kSlots) { i2 = 0; ph2 ^= 1u; }
+        if (!(ok = mbar_wait_bounded(&bar_full[i], ph, a.ctrl))) break;
+        bool have_k = false;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
           const int nt = w == 0 ? nt_a : nt_b;
-          if (t >= nt) continue;
-          if (!(ok = mbar_wait_bounded(&bar_p[w], t & 1, a.ctrl))) break;
+          if (!ok || t >= nt) continue;
+          if (!(ok = mbar_wait_bounded(&bar_p[w][0], t & 1, a.ctrl))) continue;
           tc::fence_after_sync();
-          pv(w, t);
-          if (t + 1 == nt) tc::commit(&bar_o[w]);
+          pv(w, 0, i, t > 0);
+          if (!(ok = mbar_wait_bounded(&bar_p[w][1], t & 1, a.ctrl))) continue;
+          tc::fence_after_sync();
+          pv(w, 1, i, 1u);
           if (t + 1 < nt) {
-            if (!(ok = full(2 * t + 2))) break;
-            tc::fence_after_sync();
-            qk(w, t + 1);
+            if (!have_k) {
+              if (!(ok = mbar_wait_bounded(&bar_full[i2], ph2, a.ctrl))) continue;
+              have_k = true;
+              tc::fence_after_sync();
+            }
+            qk(w, i2);
+          } else {
+            tc::commit(&bar_o[w]);
           }
         }
         if (!ok) break;
         // both tiles have taken V of tile t and K of tile t + 1
-        tc::commit(&bar_empty[(2 * t + 1) % C::kSlots]);
-        if (t + 1 < n_tiles) tc::commit(&bar_empty[(2 * t + 2) % C::kSlots]);
+        tc::commit(&bar_free[f]);
+        if (++f == 3) f = 0;
+        i = i2 + 1;
+        ph = ph2;
+        if (i == C::kSlots) { i = 0; ph ^= 1u; }
       }
     }
     __syncwarp();
@@ -363,53 +393,6 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
           for (int i = 0; i < 32; ++i)
             if (c * 32 + i > lim) s[c][i] = -INFINITY;
       }
-      float mp[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mp[j] = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) mp[i & 7] = fmaxf(mp[i & 7], fmaxf(s[c][i], s[c + 2][i]));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) mp[j] = fmaxf(mp[j], mp[j + 4]);
-      const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sl2;
-      const bool need = mx > m_ref + 8.f;
-      if (__any_sync(0xffffffffu, need)) {
-        const float m_new = need ? mx : m_ref;
-        const float alpha = need ? (m_ref == -INFINITY ? 0.f : ex2_fast(m_ref - m_new)) : 1.f;
-        if (t > 0) {
-          // (this S is complete, and the O product before it with it)
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            float o[16];
-            tc::ld16(tO(w) + lane_off + c * 16, o);
-            tc::wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= alpha;
-            tc::st16f(tO(w) + lane_off + c * 16, o);
-          }
-          tc::wait_st();
-        }
-        l *= alpha;
-        m_ref = m_new;
-      }
-      // (a row with no visible key yet, -inf - -inf, takes weight 0)
-      const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t wd[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float p0 = ex2_fast(fmaf(s[c][2 * e], sl2, nm));
-          const float p1 = ex2_fast(fmaf(s[c][2 * e + 1], sl2, nm));
-          sum[e & 3] += p0 + p1;
-          wd[e] = pack_bf16x2(p0, p1);
-        }
-        tc::st16(tS(w) + lane_off + c * 16, wd);
-      }
-      tc::wait_st();
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (key0 + 128 > sb.len) {
         // V rows past the sequence's end (both tiles' threads do this: the
         // product of either may come first)
@@ -427,8 +410,73 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
         }
         fence_proxy_async_smem();
       }
-      tc::fence_before_sync();
-      mbar_arrive(&bar_p[w]);
+      uint64_t sum[2] = {0ull, 0ull};
+      // P of 64 keys (the chunks c0, c0 + 1) for the reference m_ref, over the
+      // S columns they came from (all of S is in registers)
+      auto weights = [&](int c0) {
+        // (a row with no visible key yet, -inf - -inf, takes weight 0)
+        const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+        const uint64_t sl2_2 = f2_pack(sl2, sl2), nm_2 = f2_pack(nm, nm);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t wd[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x0 = s[c0 + c][2 * e], x1 = s[c0 + c][2 * e + 1];
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(x0, x1), sl2_2, nm_2), p0, p1);
+            p0 = ex2_fast(p0);
+            p1 = ex2_fast(p1);
+            sum[e & 1] = f2_add(sum[e & 1], f2_pack(p0, p1));
+            wd[e] = pack_bf16x2(p0, p1);
+          }
+          tc::st16(tS(w) + lane_off + (c0 + c) * 16, wd);
+        }
+      };
+      // the row maximum (eight chains of three-input maxima) moves the reference
+      // when it exceeds it by 2^8: in the first tile, and rarely later
+      float mp[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mp[j] = fmaxf(s[0][j], s[2][j]);
+#pragma unroll
+      for (int i = 8; i < 32; ++i) mp[i & 7] = max3(mp[i & 7], s[0][i], s[2][i]);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) mp[i & 7] = max3(mp[i & 7], s[1][i], s[3][i]);
+      const float mx =
+          fmaxf(max3(max3(mp[0], mp[1], mp[2]), mp[3], mp[4]), max3(mp[5], mp[6], mp[7])) * sl2;
+      const bool need = mx > m_ref + 8.f;
+      if (__any_sync(0xffffffffu, need)) {
+        const float m_new = need ? mx : m_ref;
+        const float alpha = need ? (m_ref == -INFINITY ? 0.f : ex2_fast(m_ref - m_new)) : 1.f;
+        if (t > 0) {
+          // (this S is complete, and the O product before it with it)
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+            tc::ld16(tO(w) + lane_off + c * 16, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tc::st16f(tO(w) + lane_off + c * 16, o);
+          }
+          tc::wait_st();
+        }
+        l *= alpha;
+        m_ref = m_new;
+      }
+      // each half of P is handed over by itself: its products run while the
+      // other half's exponentials do
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        weights(2 * half);
+        tc::wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&bar_p[w][half]);
+      }
+      float s0, s1, s2, s3;
+      f2_unpack(sum[0], s0, s1);
+      f2_unpack(sum[1], s2, s3);
+      l += (s0 + s1) + (s2 + s3);
     }
     if (ok && nt > 0) {
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar_o[w], 0, a.ctrl));
