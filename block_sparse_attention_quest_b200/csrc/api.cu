@@ -636,7 +636,7 @@ int resa_prefill_packed(const resa_dims* dims, const void* q, const void* k, con
   if (workspace_bytes < kCtrlBytes) return RESA_ERR_WORKSPACE;
   int Gt = 1;
   while (Gt < 8 && s.G % (2 * Gt) == 0) Gt *= 2;
-  const int64_t ctas = (total / (256 / Gt) + s.B) * (s.Hq / Gt);
+  const int64_t ctas = (total / (128 / Gt) + s.B) * (s.Hq / Gt);
   if (total > 2147483647LL - 512 || ctas > 2147483647LL) return RESA_ERR_UNSUPPORTED;
   // a CTA reads keys and values of tokens that other CTAs' outputs follow
   const size_t qb = static_cast<size_t>(total) * s.Hq * s.D * 2, kb = qb / s.G;

@@ -139,21 +139,12 @@ __device__ __forceinline__ uint32_t kv4_encode8(const float (&x)[8], float& scal
 // at a time).
 __device__ __forceinline__ uint32_t kv4_encode8(const uint4& raw, float& scale, float& zero) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  auto mn = [](uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a),
-                                     *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  };
-  auto mx = [](uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a),
-                                     *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  };
-  uint32_t lo = mn(mn(w[0], w[1]), mn(w[2], w[3])), hi = mx(mx(w[0], w[1]), mx(w[2], w[3]));
+  uint32_t lo = bf16x2_min(bf16x2_min(w[0], w[1]), bf16x2_min(w[2], w[3]));
+  uint32_t hi = bf16x2_max(bf16x2_max(w[0], w[1]), bf16x2_max(w[2], w[3]));
 #pragma unroll
   for (int m = 1; m < 8; m <<= 1) {
-    lo = mn(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-    hi = mx(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+    lo = bf16x2_min(lo, __shfl_xor_sync(0xffffffffu, lo, m));
+    hi = bf16x2_max(hi, __shfl_xor_sync(0xffffffffu, hi, m));
   }
   kv4_scale_zero(fminf(bf16_lo(lo), bf16_hi(lo)), fmaxf(bf16_lo(hi), bf16_hi(hi)), scale, zero);
   float x[8];

@@ -5,30 +5,29 @@
 //   out_i = sum_{t <= i} softmax_t(scale q_i . k_t) v_t   inside each sequence
 //
 // Sequence b is tokens starts[b] .. starts[b + 1] - 1 of q, k and v. A CTA
-// takes 256 rows of one sequence: 256 / Gt consecutive queries of Gt query
-// heads that share a KV head (Gt: the largest power of two that divides the
-// group), as two 128-row tiles A and B (M = 128, row = query * Gt + head,
-// which is how q lies in memory), and walks the key tiles of 128 tokens up to
-// its last query. Both tiles use every K and V tile that arrives, so a tile is
-// read from L2 once for 256 rows. Bound: the tensor cores and, equally, the
-// exponential unit (2 x 128 x 128 exponentials take 2048 cycles of an SM, as
-// do the four 128^3 products).
+// takes NT = 2 (or 1) tiles of 128 rows of one sequence: row = query * Gt +
+// head, of 128 / Gt consecutive queries of Gt query heads that share a KV head
+// (Gt: the largest power of two that divides the group), which is how q lies
+// in memory; and walks the key tiles of 128 tokens up to its last query. Both
+// tiles use every K and V tile that arrives, so a tile is read from L2 once
+// for 256 rows. Bound: the tensor cores and, equally, the exponential unit
+// (2 x 128 x 128 exponentials take 2048 cycles of an SM, as do the four 128^3
+// products).
 //
-// 12 warps:
-//   0-3, 4-7  softmax of tile A and of tile B, one row per thread (= TMEM
-//             lane): S is read into registers whole, the row maximum moves
-//             its reference only when it grows by more than 2^8 (O is
-//             rescaled in TMEM then), and P = 2^(s - m) goes back as bf16
-//             over the S columns, as the A operand of the second product;
-//   8         one thread issues the products. For each tile the next S is
+// NT + 1 warpgroups:
+//   NT softmax warpgroups, one tile each, one row per thread (= TMEM lane): S
+//             is read into registers whole, the row maximum moves its
+//             reference only when it grows by more than 2^8 (O is rescaled in
+//             TMEM then), and P = 2^(s - m) goes back as bf16 over the S
+//             columns, as the A operand of the second product;
+//   4 warps:  one thread issues the products. For each tile the next S is
 //             issued right behind the O product that reads the previous P
 //             from the same columns: the tensor pipe runs them in order. Its
-//             completion therefore also says that O may be rescaled;
-//   9         one thread issues the TMA copies: Q, then K and V tiles through a
-//             ring of five 128-token slots;
-//   10        copies this CTA's own tokens of K and V from the packed tensors to the
-//             caches and writes their block descriptors (one CTA per KV head);
-//   11        idle (registers are handed over by whole warpgroups).
+//             completion therefore also says that O may be rescaled.
+//             One thread issues the TMA copies: Q, then K and V tiles through
+//             a ring of 128-token slots. Two warps copy this CTA's own tokens
+//             of K and V from the packed tensors to the caches and write their
+//             block descriptors (one CTA per KV head).
 // While one tile's softmax runs, the other tile's products do.
 //
 // Rows of a key tile past the sequence's end belong to other sequences: their
@@ -50,23 +49,31 @@ struct PackedK {
   Ctrl* ctrl;
   int64_t L_max;
   int Mmax;
-  int B, T, longest, Hq, H, G, Gt;
+  int B, T, longest, Hq, H, G;
+  int gs;                     // Gt = 1 << gs
   float scale_log2;
 };
 
-template <int D>
+// NT: 128-row tiles per CTA. Two, one CTA per SM, for long sequences; one, two
+// CTAs per SM, for short ones, whose CTAs spend most of their time on the way
+// to the first product and from the last (about 7 us; the other CTA's work
+// fills it).
+template <int D, int NT>
 struct PackedCfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kHalfBytes = 128 * 128;          // [128 rows][64 bf16]
   static constexpr int kTileBytes = kHalves * kHalfBytes;
-  static constexpr int kSlots = 5;
-  // (at least 116 KB: a second CTA on the SM would wait for TMEM columns)
-  static constexpr int kNeed = (2 + kSlots) * kTileBytes + 1024;
-  static constexpr int kSmem = kNeed > 116 * 1024 ? kNeed : 116 * 1024;
-  // twelve warps start with 168 registers each; the softmax warps, which hold
-  // a row of S, take 200, the third warpgroup leaves them (2 * 200 + 104 = 3 * 168)
-  static constexpr int kThreads = 12 * 32;
-  static constexpr int kRegsSoftmax = 200, kRegsOther = 104;
+  static constexpr int kSlots = NT == 2 || D == 64 ? 5 : 2;
+  // (never room for more CTAs than have their TMEM columns: one would wait)
+  static constexpr int kLeast = NT == 2 ? 116 * 1024 : 78 * 1024;
+  static constexpr int kNeed = (NT + kSlots) * kTileBytes + 1024;
+  static constexpr int kSmem = kNeed > kLeast ? kNeed : kLeast;
+  static constexpr uint32_t kTmemCols = 256 * NT;        // S and O of each tile, 128 columns each
+  // The warps start with 168 registers each (NT = 2, twelve warps) or 128; the
+  // softmax warps, which hold a row of S, take 200, the last warpgroup leaves
+  // them (2 * 200 + 104 = 3 * 168, 200 + 56 = 2 * 128).
+  static constexpr int kThreads = (NT + 1) * 128;
+  static constexpr int kRegsSoftmax = 200, kRegsOther = NT == 2 ? 104 : 56;
 };
 
 __device__ __forceinline__ float ex2_fast(float x) {
@@ -96,117 +103,122 @@ __device__ __forceinline__ SeqBounds seq_bounds(const PackedK& a, int b) {
   return r;
 }
 
-// K and V rows [t0, t0 + n) of a sequence to its cache row, and the
-// descriptors of their blocks (t0 is a multiple of 16); one warp.
+// V, or K, rows [t0, t0 + n) of a sequence to its cache row, with K the
+// descriptors of their blocks (t0 is a multiple of 16); one warp each.
 template <int D>
-__device__ __forceinline__ void fill_cache(const PackedK& a, int b, int begin, int g, int t0,
-                                           int n) {
+__device__ __forceinline__ void fill_cache(const PackedK& a, bool is_v, int b, int begin, int g,
+                                           int t0, int n) {
   constexpr int CPR = D / 8, TPP = 32 / CPR, NP = kBlock / TPP;
   const int lane = threadIdx.x & 31, chunk = lane % CPR, r0 = lane / CPR;
   const int64_t bh = static_cast<int64_t>(b) * a.H + g;
   const int64_t stride = static_cast<int64_t>(a.H) * D;
-  const __nv_bfloat16* ks = a.k + (static_cast<int64_t>(begin + t0) * a.H + g) * D + chunk * 8;
-  const __nv_bfloat16* vs = a.v + (static_cast<int64_t>(begin + t0) * a.H + g) * D + chunk * 8;
+  __nv_bfloat16* cache = is_v ? a.v_cache : a.k_cache;
+  if (cache == nullptr && (is_v || a.desc == nullptr)) return;
+  const __nv_bfloat16* src =
+      (is_v ? a.v : a.k) + (static_cast<int64_t>(begin + t0) * a.H + g) * D + chunk * 8;
+  __nv_bfloat16* dst = cache + (bh * a.L_max + t0) * D + chunk * 8;
 #pragma unroll 1
   for (int j = 0; j < n; j += kBlock) {
     const int valid = n - j < kBlock ? n - j : kBlock;
     uint4 x[NP];
-    if (a.v_cache != nullptr) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
-        if (r0 + i * TPP < valid) x[i] = ldg16(vs + (j + r0 + i * TPP) * stride);
+    for (int i = 0; i < NP; ++i)
+      if (r0 + i * TPP < valid) x[i] = ldg16(src + (j + r0 + i * TPP) * stride);
+    if (cache != nullptr) {
 #pragma unroll
       for (int i = 0; i < NP; ++i)
         if (r0 + i * TPP < valid)
-          *reinterpret_cast<uint4*>(a.v_cache + (bh * a.L_max + t0 + j + r0 + i * TPP) * D +
-                                    chunk * 8) = x[i];
+          *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(j + r0 + i * TPP) * D) = x[i];
     }
+    if (is_v || a.desc == nullptr) continue;
+    // (bf16 minima and maxima, two at a time: exact)
+    uint32_t mn[4], mx[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { mn[e] = 0x7f807f80u; mx[e] = 0xff80ff80u; }
+    auto fold = [&](uint32_t (&lo)[4], uint32_t (&hi)[4], const uint32_t (&u)[4], const uint32_t (&v)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        lo[e] = bf16x2_min(lo[e], u[e]);
+        hi[e] = bf16x2_max(hi[e], v[e]);
+      }
+    };
 #pragma unroll
     for (int i = 0; i < NP; ++i)
-      if (r0 + i * TPP < valid) x[i] = ldg16(ks + (j + r0 + i * TPP) * stride);
-    float mn[8], mx[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) { mn[e] = INFINITY; mx[e] = -INFINITY; }
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
       if (r0 + i * TPP < valid) {
-        if (a.k_cache != nullptr)
-          *reinterpret_cast<uint4*>(a.k_cache + (bh * a.L_max + t0 + j + r0 + i * TPP) * D +
-                                    chunk * 8) = x[i];
-        float f[8];
-        Chunk<__nv_bfloat16>::unpack(x[i], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) { mn[e] = fminf(mn[e], f[e]); mx[e] = fmaxf(mx[e], f[e]); }
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        fold(mn, mx, w, w);
       }
+#pragma unroll
+    for (int m = CPR; m < 32; m <<= 1) {
+      uint32_t u[4], v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u[e] = __shfl_xor_sync(0xffffffffu, mn[e], m);
+        v[e] = __shfl_xor_sync(0xffffffffu, mx[e], m);
+      }
+      fold(mn, mx, u, v);
     }
-    if (a.desc == nullptr) continue;
-#pragma unroll
-    for (int m = CPR; m < 32; m <<= 1)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        mn[e] = fminf(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], m));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], m));
-      }
     if (lane < CPR) {
       __nv_bfloat16* d = a.desc + (bh * a.Mmax + (t0 + j) / kBlock) * 2 * D + chunk * 8;
-      *reinterpret_cast<uint4*>(d) = Chunk<__nv_bfloat16>::pack(mn);
-      *reinterpret_cast<uint4*>(d + D) = Chunk<__nv_bfloat16>::pack(mx);
+      *reinterpret_cast<uint4*>(d) = make_uint4(mn[0], mn[1], mn[2], mn[3]);
+      *reinterpret_cast<uint4*>(d + D) = make_uint4(mx[0], mx[1], mx[2], mx[3]);
     }
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
+template <int D, int NT>
+__global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2))
     prefill_packed_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV, PackedK a) {
-  using C = PackedCfg<D>;
+  using C = PackedCfg<D, NT>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_q[2], bar_full[C::kSlots], bar_free[3];
-  __shared__ __align__(8) uint64_t bar_s[2], bar_p[2][2], bar_o[2];   // [tile], P: [tile][half of the keys]
+  __shared__ __align__(8) uint64_t bar_q[NT], bar_full[C::kSlots], bar_free[3];
+  __shared__ __align__(8) uint64_t bar_s[NT], bar_p[NT][2], bar_o[NT];   // [tile], P: [tile][half of the keys]
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int s_seq, s_block;
+  __shared__ int s_seq, s_block, s_tot[C::kThreads / 32];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   auto sQ = [&](int w) { return base + w * C::kTileBytes; };
-  auto slot = [&](int n) { return base + (2 + n % C::kSlots) * C::kTileBytes; };
+  auto slot = [&](int n) { return base + (NT + n % C::kSlots) * C::kTileBytes; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int QT = 128 / a.Gt, QB = 2 * QT;         // queries per tile, per CTA
-  const int n_hg = a.Hq / a.Gt;
+  const int Gt = 1 << a.gs, QT = 128 >> a.gs, QB = NT * QT;   // queries per tile, per CTA
+  const int qbs = 7 - a.gs + (NT - 1);            // QB = 1 << qbs
+  const int n_hg = a.Hq >> a.gs;
   const int hg = blockIdx.x % n_hg, x = blockIdx.x / n_hg;
 
   // which sequence and which of its query blocks (the last ones, which see the
-  // most keys, first)
-  if (warp == 0) {
-    int run = 0, seq = -1, blk = 0;
-    for (int b0 = 0; b0 < a.B && seq < 0; b0 += 32) {
-      const int b = b0 + lane;
-      int n = 0;
-      if (b < a.B) {
-        const SeqBounds sb = seq_bounds(a, b);
-        n = (sb.len + QB - 1) / QB;
-        if (blockIdx.x == 0 && sb.bad) raise_error(a.ctrl, kErrBadIndex);
-      }
-      int inc = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      const bool here = x >= run + inc - n && x < run + inc;
-      const unsigned who = __ballot_sync(0xffffffffu, here);
-      if (who) {
-        const int src = __ffs(who) - 1;
-        seq = b0 + src;
-        blk = __shfl_sync(0xffffffffu, run + inc - 1 - x, src);
-      }
-      run += __shfl_sync(0xffffffffu, inc, 31);
+  // most keys, first): one sequence per thread, a scan of their block counts
+  if (threadIdx.x == 0) s_seq = -1;
+  for (int b0 = 0, run = 0; b0 < a.B; b0 += C::kThreads) {
+    const int b = b0 + threadIdx.x;
+    int n = 0;
+    if (b < a.B) {
+      const SeqBounds sb = seq_bounds(a, b);
+      n = (sb.len + QB - 1) >> qbs;
+      if (blockIdx.x == 0 && sb.bad) raise_error(a.ctrl, kErrBadIndex);
     }
-    // (the first CTA looks at every entry, to report a bad one)
-    if (blockIdx.x == 0)
-      for (int b = lane; b < a.B; b += 32)
-        if (seq_bounds(a, b).bad) raise_error(a.ctrl, kErrBadIndex);
-    if (lane == 0) { s_seq = seq; s_block = blk; }
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();                              // (the last round's totals are read)
+    if (lane == 31) s_tot[warp] = inc;
+    __syncthreads();
+    int before = run, all = run;
+#pragma unroll
+    for (int i = 0; i < C::kThreads / 32; ++i) {
+      before += i < warp ? s_tot[i] : 0;
+      all += s_tot[i];
+    }
+    if (x >= before + inc - n && x < before + inc) {
+      s_seq = b;
+      s_block = before + inc - 1 - x;
+    }
+    run = all;
+    if (run > x && blockIdx.x != 0) break;        // (the first CTA reports every bad entry)
   }
   __syncthreads();
   const int b = s_seq;
@@ -214,15 +226,15 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
   const SeqBounds sb = seq_bounds(a, b);
   const int q0 = s_block * QB;
   const int nq = sb.len - q0 < QB ? sb.len - q0 : QB;
-  const int g = hg * a.Gt / a.G;                  // KV head
+  const int g = (hg << a.gs) / a.G;                  // KV head
   // key tiles of A and of B (none without queries)
   const int nt_a = (q0 + (nq < QT ? nq : QT) - 1) / 128 + 1;
-  const int nt_b = nq > QT ? (q0 + nq - 1) / 128 + 1 : 0;
+  const int nt_b = NT > 1 && nq > QT ? (q0 + nq - 1) / 128 + 1 : 0;
   const int n_tiles = nt_b > nt_a ? nt_b : nt_a;
 
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < NT; ++w) {
       mbar_init(&bar_q[w], 1);
       mbar_init(&bar_s[w], 1);
       mbar_init(&bar_p[w][0], 128);
@@ -237,17 +249,17 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
     for (int i = 0; i < 3; ++i) mbar_init(&bar_free[i], 1);
     fence_mbar_init();
   }
-  if (warp == 8) tc::alloc(&tmem_base_sh, 512);
+  if (warp == 4 * NT) tc::alloc(&tmem_base_sh, C::kTmemCols);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tmem_base_sh;
   auto tS = [&](int w) { return tmem + 128u * w; };
-  auto tO = [&](int w) { return tmem + 256u + 128u * w; };
+  auto tO = [&](int w) { return tmem + 128u * NT + 128u * w; };
 
-  if (warp >= 8) {
+  if (warp >= 4 * NT) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
-  if (warp == 9) {
+  if (warp == 4 * NT + 1) {
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
       prefetch_tmap(&tmQ);
@@ -257,7 +269,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
         mbar_arrive_expect_tx(&bar_q[w], C::kTileBytes);
 #pragma unroll
         for (int hf = 0; hf < C::kHalves; ++hf)
-          tma_load_3d(sQ(w) + hf * C::kHalfBytes, &tmQ, hf * 64, hg * a.Gt, sb.begin + q0 + w * QT,
+          tma_load_3d(sQ(w) + hf * C::kHalfBytes, &tmQ, hf * 64, hg << a.gs, sb.begin + q0 + w * QT,
                       &bar_q[w]);
       };
       load_q(0);
@@ -277,7 +289,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
         for (int hf = 0; hf < C::kHalves; ++hf)
           tma_load_3d(slot(n) + hf * C::kHalfBytes, map, hf * 64, g, sb.begin + (n >> 1) * 128,
                       &bar_full[i]);
-        if (n == 0 && nt_b > 0) load_q(1);
+        if (NT > 1 && n == 0 && nt_b > 0) load_q(NT - 1);
       }
       if (!ok) {
         // the copies in flight end (within the bound) before this CTA does
@@ -286,7 +298,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 8) {
+  } else if (warp == 4 * NT) {
     // -------------------------------------------------------------- products
     if (lane == 0) {
       constexpr uint32_t idS = tc::idesc_bf16(128, 128, false);
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
         if (!(ok = mbar_wait_bounded(&bar_full[i], ph, a.ctrl))) break;
         bool have_k = false;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < NT; ++w) {
           const int nt = w == 0 ? nt_a : nt_b;
           if (!ok || t >= nt) continue;
           if (!(ok = mbar_wait_bounded(&bar_p[w][0], t & 1, a.ctrl))) continue;
@@ -359,10 +371,9 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if ((hg << a.gs) % a.G == 0) {
     // ------------------------------------------------- caches and descriptors
-    if (hg * a.Gt % a.G == 0 && (a.k_cache != nullptr || a.desc != nullptr))
-      fill_cache<D>(a, b, sb.begin, g, q0, nq);
+    fill_cache<D>(a, warp == 4 * NT + 3, b, sb.begin, g, q0, nq);
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
@@ -370,7 +381,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
     const int w = warp >> 2;
     const int nt = w == 0 ? nt_a : nt_b;
     const int row = threadIdx.x & 127;             // TMEM lane
-    const int qpos = q0 + w * QT + row / a.Gt;     // causal limit
+    const int qpos = q0 + w * QT + (row >> a.gs);     // causal limit
     const int qpos_lo = q0 + w * QT;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float sl2 = a.scale_log2;
@@ -507,9 +518,9 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
         for (int it = 0; it < 32 / RPI; ++it) {
           const int r = it * RPI + lane / NU;
           const int rt = (warp & 3) * 32 + r;      // row of the tile
-          const int qi = w * QT + rt / a.Gt;
+          const int qi = w * QT + (rt >> a.gs);
           if (qi >= nq) continue;
-          const int64_t orow = static_cast<int64_t>(sb.begin + q0 + qi) * a.Hq + hg * a.Gt + rt % a.Gt;
+          const int64_t orow = static_cast<int64_t>(sb.begin + q0 + qi) * a.Hq + (hg << a.gs) + (rt & (Gt - 1));
           *reinterpret_cast<uint4*>(a.out + orow * D + j * 8) = st[r * NU + (j ^ (r & 7))];
         }
       }
@@ -517,21 +528,21 @@ __global__ void __launch_bounds__(PackedCfg<D>::kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 4 * NT) {
     tc::fence_after_sync();
-    tc::dealloc(tmem, 512);
+    tc::dealloc(tmem, C::kTmemCols);
   }
 }
 
-template <int D>
+template <int D, int NT>
 static cudaError_t prefill_packed_t(const PackedArgs& r, cudaStream_t st) {
-  using C = PackedCfg<D>;
+  using C = PackedCfg<D, NT>;
   static std::atomic<bool> attr_set[64];   // per device; launches may come from several host threads
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_packed_kernel<D>,
+    cudaError_t e = cudaFuncSetAttribute(prefill_packed_kernel<D, NT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
@@ -546,18 +557,26 @@ static cudaError_t prefill_packed_t(const PackedArgs& r, cudaStream_t st) {
   k.desc = static_cast<__nv_bfloat16*>(r.desc);
   k.ctrl = r.ctrl;
   k.L_max = r.L_max; k.Mmax = static_cast<int>(r.L_max / kBlock);
-  k.B = r.B; k.T = r.T; k.longest = r.longest; k.Hq = r.Hq; k.H = r.H; k.G = r.G; k.Gt = r.Gt;
+  k.B = r.B; k.T = r.T; k.longest = r.longest; k.Hq = r.Hq; k.H = r.H; k.G = r.G;
+  while ((1 << k.gs) < r.Gt) ++k.gs;
   k.scale_log2 = r.scale * 1.4426950408889634f;
   // every sequence has at most one query block that is not full
-  const int QB = 256 / r.Gt;
+  const int QB = NT * 128 / r.Gt;
   const int64_t blocks = r.T / QB + r.B;
-  prefill_packed_kernel<D><<<static_cast<unsigned>(blocks * (r.Hq / r.Gt)), C::kThreads, C::kSmem, st>>>(
+  prefill_packed_kernel<D, NT><<<static_cast<unsigned>(blocks * (r.Hq / r.Gt)), C::kThreads, C::kSmem, st>>>(
       *r.tm_q, *r.tm_k, *r.tm_v, k);
   return cudaGetLastError();
 }
 
+// One or two tiles per CTA, measured on 16384 tokens of equal sequences (32/8
+// heads, d = 128; us with one, with two): 32 tokens 176, 256; 100: 148, 168;
+// 256: 130, 136; 512: 156, 160; 1024: 208, 208; 2048: 316, 307; 4096: 540, 515;
+// 16384: 2150, 1863. A batch counts as long by its mean, or by one long
+// sequence, which then holds most of the work.
 cudaError_t launch_prefill_packed(const PackedArgs& r, cudaStream_t st) {
-  return r.D == 128 ? prefill_packed_t<128>(r, st) : prefill_packed_t<64>(r, st);
+  const bool two = r.longest > 2048 || r.T / r.B > 1024;
+  if (r.D == 128) return two ? prefill_packed_t<128, 2>(r, st) : prefill_packed_t<128, 1>(r, st);
+  return two ? prefill_packed_t<64, 2>(r, st) : prefill_packed_t<64, 1>(r, st);
 }
 
 }  // namespace resa

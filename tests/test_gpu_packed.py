@@ -97,10 +97,11 @@ def starts_of(lens, lead=0):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 6, 8])
 @pytest.mark.parametrize("lens", [[1], [128], [1, 0, 31, 33, 200], [63, 64, 65, 127, 129], [300, 257]])
-def test_packed(resa, d, G, lens):
+@pytest.mark.parametrize("longest", [None, 2100])       # (one tile per CTA, two)
+def test_packed(resa, d, G, lens, longest):
     H, st = 2, starts_of(lens)
     q, k, v = rnd(1, st[-1], H * G, d), rnd(2, st[-1], H, d), rnd(3, st[-1], H, d)
-    out, kc, vc, ds, ws, scale = call(resa, q, k, v, st, 320)
+    out, kc, vc, ds, ws, scale = call(resa, q, k, v, st, 320 if longest is None else 2112, longest)
     assert resa.workspace_status(ws) == resa.RESA_OK
     check(resa, q, k, v, st, out, kc, vc, ds, scale)
 
@@ -117,32 +118,35 @@ def test_rows_before_and_behind_the_sequences_stay(resa):
     assert resa.workspace_status(ws) == resa.RESA_OK
 
 
+@pytest.mark.parametrize("short", [True, False])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_values_of_a_neighbour_do_not_leak(resa, bad):
+def test_values_of_a_neighbour_do_not_leak(resa, bad, short):
     """Keys, values and queries of one sequence that are not finite change no
     bit of another's outputs, though their key tiles hold rows of both."""
     lens = [50, 77, 30, 129]
     st = starts_of(lens)
     q, k, v = rnd(1, st[-1], 8, 64), rnd(2, st[-1], 2, 64), rnd(3, st[-1], 2, 64)
-    clean = call(resa, q, k, v, st, 144)[0]
+    cap, longest = (144, None) if short else (2112, 2100)
+    clean = call(resa, q, k, v, st, cap, longest)[0]
     q2, k2, v2 = q.copy(), k.copy(), v.copy()
     for x in (q2, k2, v2):
         x[st[1]:st[2]] = bad
         x[st[3] + 128:] = bad                       # behind the last sequence's first tile
-    out = call(resa, q2, k2, v2, st, 144)[0]
+    out = call(resa, q2, k2, v2, st, cap, longest)[0]
     for i in (0, 2):
         assert torch.equal(out[st[i]:st[i + 1]], clean[st[i]:st[i + 1]])
     assert torch.equal(out[st[3]:st[3] + 128], clean[st[3]:st[3] + 128])
 
 
-def test_large_logits(resa):
+@pytest.mark.parametrize("longest", [None, 2100])
+def test_large_logits(resa, longest):
     """Logits of some hundreds: maxima that grow along the row (rescaling), and
     weights that vanish."""
     n = 700
     q, k, v = rnd(1, n, 4, 128), rnd(2, n, 1, 128), rnd(3, n, 1, 128)
     k *= np.linspace(0.1, 16, n).astype(np.float32)[:, None, None]
     k = ops.bf16_round(k)
-    out, kc, vc, ds, ws, scale = call(resa, q, k, v, [0, n], 704, scale=1.0)
+    out, kc, vc, ds, ws, scale = call(resa, q, k, v, [0, n], 2112, longest, scale=1.0)
     o = out.double().cpu().numpy()
     for h in range(4):
         z = q[:, h].astype(np.float64) @ k[:, 0].astype(np.float64).T
