@@ -345,6 +345,12 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                   *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // ---------------------------------------------------------------- reductions
 __device__ __forceinline__ float warp_max_xor(float v, int from, int to) {
   for (int m = from; m >= to; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));

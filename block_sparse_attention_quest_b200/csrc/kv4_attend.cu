@@ -50,6 +50,8 @@ struct Kv4K {
   int n_min;
   int B, H, G, Mmax, n_sel;
   int splits;              // parts per (row, head) with a CTA each, or 0: parts of the range
+  int row_blocks;          // with splits: the blocks of every (row, head), their
+  int split_per, split_rem;   // quotient and rest by splits
   float scale_log2;
 };
 
@@ -280,12 +282,12 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
   Kv4Range range;
   uint32_t x = 0, part1 = 0, row_start = 0, m_row;
   int row;
-  if (a.splits > 0) {
-    m_row = kv4_row_blocks(a, 0);
-    row = static_cast<int>(blockIdx.x) / (a.splits * a.H);
+  if (a.splits > 0) {                             // grid (splits, H, B)
+    m_row = a.row_blocks;
+    row = blockIdx.z;
   } else {
     if (a.lens == nullptr) {
-      m_row = kv4_row_blocks(a, 0);
+      m_row = a.row_blocks;
       const uint32_t per_row = a.H * (m_row + kKv4PieceCost);
       range.set(per_row * a.B, gridDim.x);
       if (static_cast<int>(blockIdx.x) >= range.ctas) return;
@@ -363,16 +365,16 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     if (a.splits > 0) {
       if (x != 0) return false;
       x = 1;
-      const int part = static_cast<int>(blockIdx.x) % a.splits;
-      g = static_cast<int>(blockIdx.x) / a.splits % a.H;
-      const int per = m_row / a.splits, rem = m_row % a.splits;
-      i0 = part * per + min(part, rem);
-      i1 = i0 + per + (part < rem);
+      const int part = blockIdx.x;
+      g = blockIdx.y;
+      i0 = part * a.split_per + min(part, a.split_rem);
+      i1 = i0 + a.split_per + (part < a.split_rem);
       bh = static_cast<int64_t>(row) * a.H + g;
       if (threadIdx.x == 0) {
         done.bh = bh;
-        done.slot = a.splits == 1 ? -1 : 2 * static_cast<int>(blockIdx.x);
-        done.first = static_cast<int>(blockIdx.x) - part; done.parts = a.splits; done.late = 0;
+        done.first = static_cast<int>(bh) * a.splits;
+        done.slot = a.splits == 1 ? -1 : 2 * (done.first + part);
+        done.parts = a.splits; done.late = 0;
       }
     } else {
       uint32_t u0, u1, from;
@@ -423,31 +425,52 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     uint32_t qb[PARTS][NG * 4][2];
     float qs0[NG], qs1[NG];
     {
-      const T* qg = static_cast<const T*>(a.q) + bh * a.G * D;
+      const T* qg = static_cast<const T*>(a.q) + (bh * a.G + gq) * D + cq * 16;
+      // word j: product step 2j takes nibbles 0, 4 and 1, 5 (the latter read 16
+      // times too large), step 2j + 1 nibbles 2, 6 and 3, 7
 #pragma unroll
       for (int g2 = 0; g2 < NG; ++g2) {
         float sum = 0.f;
+        if constexpr (PARTS == 1) {
+          uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+          if (gq < a.G) {
+            raw[0] = ldg16(qg + g2 * 64);
+            raw[1] = ldg16(qg + g2 * 64 + 8);
+          }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float f[8];
+          for (int j = 0; j < 2; ++j) {
+            float f[8];
+            Chunk<__nv_bfloat16>::unpack(raw[j], f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = 0.f;
-          if (gq < a.G) load8<T>(qg + gq * D + g2 * 64 + cq * 16 + j * 8, f);
+            for (int i = 0; i < 8; ++i) sum += f[i];
+            const uint32_t lo[2] = {raw[j].x, raw[j].y}, hi[2] = {raw[j].z, raw[j].w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum += f[i];
-          float part[8][PARTS];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) bf16_parts<PARTS>(f[i] * kUp, part[i]);
-          // word j: product step 2j takes nibbles 0, 4 and 1, 5 (the latter
-          // read 16 times too large), step 2j + 1 nibbles 2, 6 and 3, 7
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              qb[p][g2 * 4 + 2 * j + s][0] = pack_bf16x2(part[2 * s][p], part[2 * s + 4][p]);
-              qb[p][g2 * 4 + 2 * j + s][1] =
-                  pack_bf16x2(part[2 * s + 1][p] * 0.0625f, part[2 * s + 5][p] * 0.0625f);
+            for (int s = 0; s < 2; ++s) {          // times 2^64 and 2^60, exact
+              qb[0][g2 * 4 + 2 * j + s][0] = bf16x2_mul(__byte_perm(lo[s], hi[s], 0x5410), 0x5f805f80u);
+              qb[0][g2 * 4 + 2 * j + s][1] = bf16x2_mul(__byte_perm(lo[s], hi[s], 0x7632), 0x5d805d80u);
             }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = 0.f;
+            if (gq < a.G) load8<T>(qg + g2 * 64 + j * 8, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += f[i];
+            float part[8][PARTS];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) bf16_parts<PARTS>(f[i] * kUp, part[i]);
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+              for (int s = 0; s < 2; ++s) {
+                qb[p][g2 * 4 + 2 * j + s][0] = pack_bf16x2(part[2 * s][p], part[2 * s + 4][p]);
+                qb[p][g2 * 4 + 2 * j + s][1] =
+                    pack_bf16x2(part[2 * s + 1][p] * 0.0625f, part[2 * s + 5][p] * 0.0625f);
+              }
+          }
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -707,21 +730,28 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     __syncthreads();
     const Kv4Done dn = s_done[piece & 1];
     T* out = static_cast<T*>(a.out);
-    for (int i = threadIdx.x; i < a.G * D; i += NW * 32) {
-      const int h = i / D, ch = i % D;
-      float v = 0.f;
+    for (int i = threadIdx.x; i < a.G * (D / 2); i += NW * 32) {
+      const int h = i / (D / 2), ch = (i % (D / 2)) * 2;
+      float v0 = 0.f, v1 = 0.f;
 #pragma unroll 4
-      for (int w = 0; w < NW; ++w) v = fmaf(sm_m[w * 8 + h], sm_o[(w * 8 + h) * OR + ch], v);
+      for (int w = 0; w < NW; ++w) {
+        const float sc = sm_m[w * 8 + h];
+        const float2 y = *reinterpret_cast<const float2*>(sm_o + (w * 8 + h) * OR + ch);
+        v0 = fmaf(sc, y.x, v0);
+        v1 = fmaf(sc, y.y, v1);
+      }
       if (dn.slot < 0) {
-        out[(dn.bh * a.G + h) * D + ch] = Dt<T>::from_f(v / s_l[h]);
+        const float inv = 1.f / s_l[h];
+        out[(dn.bh * a.G + h) * D + ch] = Dt<T>::from_f(v0 * inv);
+        out[(dn.bh * a.G + h) * D + ch + 1] = Dt<T>::from_f(v1 * inv);
         if (a.lse != nullptr && ch == 0)
           a.lse[dn.bh * a.G + h] = (s_mx[h] + log2f(s_l[h])) * 0.69314718055994531f;
       } else {
-        a.part_o[(static_cast<int64_t>(dn.slot) * a.G + h) * D + ch] = v;
-        if (ch == 0) {
-          a.part_ml[(dn.slot * a.G + h) * 2] = s_mx[h];
-          a.part_ml[(dn.slot * a.G + h) * 2 + 1] = s_l[h];
-        }
+        *reinterpret_cast<float2*>(a.part_o + (static_cast<int64_t>(dn.slot) * a.G + h) * D + ch) =
+            make_float2(v0, v1);
+        if (ch == 0)
+          *reinterpret_cast<float2*>(a.part_ml + (dn.slot * a.G + h) * 2) =
+              make_float2(s_mx[h], s_l[h]);
       }
     }
     __syncthreads();
@@ -752,7 +782,7 @@ static cudaError_t kv4_attend_t(const Shape& s, const Kv4K& k, int ctas, cudaStr
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = k.splits > 0 ? dim3(k.splits, k.H, k.B) : dim3(ctas);
   cfg.blockDim = dim3(kKv4Warps<T> * 32);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
@@ -806,6 +836,11 @@ cudaError_t launch_kv4_attend(const Shape& s, const Kv4Args& a, cudaStream_t st)
   k.out = a.out; k.lse = a.lse; k.len = a.len; k.r = a.r; k.n_min = a.n_min;
   k.B = s.B; k.H = s.H; k.G = s.G; k.splits = a.splits; k.Mmax = s.Mmax; k.n_sel = a.n_sel;
   k.scale_log2 = a.scale * 1.4426950408889634f;
+  k.row_blocks = a.sel ? a.n_sel : static_cast<int>((a.len + kBlock - 1) / kBlock);
+  if (a.splits > 0) {
+    k.split_per = k.row_blocks / a.splits;
+    k.split_rem = k.row_blocks % a.splits;
+  }
   if (s.bf16) return s.D == 128 ? kv4_attend_d<__nv_bfloat16, 128>(s, k, a.ctas, st)
                                 : kv4_attend_d<__nv_bfloat16, 64>(s, k, a.ctas, st);
   return s.D == 128 ? kv4_attend_d<float, 128>(s, k, a.ctas, st)
