@@ -63,17 +63,18 @@ __device__ __forceinline__ void load8<float>(const float* p, float (&f)[8]) {
 }
 
 // Eight codes (nibble i = channel i) of x for a group's scale and zero:
-// rint(fl((x - zero) / scale)), with inv = fl(1 / scale).
+// rint(fl((x - zero) / scale)), with inv = 1 / scale to one unit in the last
+// place.
 //
 // The rounded quotient comes without a division. With d = fl(x - zero) and
 // q0 = fl(d inv), which is within 2^-22 of d / scale relatively, the residual
 // d - q0 scale is exact in one fused operation (scale has 8 significant bits,
 // so q0 scale has 32, of which the upper 22 cancel), and q0 + residual inv is
-// within 2^-45 of the quotient before its one rounding. A quotient of a 24-bit
+// within 2^-44 of the quotient before its one rounding. A quotient of a 24-bit
 // by an 8-bit number that is not itself half-way between two fp32 numbers is
 // at least 2^-34 away from there, so that rounding is the quotient's. This
-// needs inv and the residual to be normal numbers: scales below 1e-30 take
-// the division (a constant group's scale is 0, its codes are 0).
+// needs inv and the residual to be normal numbers: scales outside 1e-30 ..
+// 1e30 take the division (a constant group's scale is 0, its codes are 0).
 //
 // EXACT_ZERO: x holds bf16 values, whose minimum the zero is; then no quotient
 // leaves [0, 15.5) and nothing is clamped.
@@ -84,7 +85,10 @@ __device__ __forceinline__ uint32_t kv4_codes8(const float (&x)[8], float scale,
   const uint64_t nz = f2_pack(-zero, -zero), iv = f2_pack(inv, inv);
   const uint64_t ns = f2_pack(-scale, -scale);
   const uint64_t up = f2_pack(kMagic, kMagic), down = f2_pack(-kMagic, -kMagic);
-  float c[8];
+  // (2^23 on the pairs' first halves: the sums below then hold the codes in
+  // their low bits)
+  const uint64_t down0 = f2_pack(8388608.f - kMagic, -kMagic), k256 = f2_pack(256.f, 256.f);
+  uint64_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint64_t d = f2_add(f2_pack(x[2 * i], x[2 * i + 1]), nz);
@@ -95,13 +99,15 @@ __device__ __forceinline__ uint32_t kv4_codes8(const float (&x)[8], float scale,
       f2_unpack(q, a, b);
       q = f2_pack(fminf(fmaxf(a, 0.f), 15.f), fminf(fmaxf(b, 0.f), 15.f));
     }
-    f2_unpack(f2_add(f2_add(q, up), down), c[2 * i], c[2 * i + 1]);
+    c[i] = f2_add(f2_add(q, up), i & 1 ? down : down0);
   }
   // four codes at a time as one number below 2^16, exact in fp32
-  const float lo = fmaf(fmaf(fmaf(c[3], 16.f, c[2]), 16.f, c[1]), 16.f, c[0]);
-  const float hi = fmaf(fmaf(fmaf(c[7], 16.f, c[6]), 16.f, c[5]), 16.f, c[4]);
-  uint32_t w = __byte_perm(__float_as_uint(lo + 8388608.f), __float_as_uint(hi + 8388608.f), 0x5410);
-  if (!(scale > 1e-30f)) {
+  float e0, o0, e1, o1;
+  f2_unpack(f2_fma(c[1], k256, c[0]), e0, o0);
+  f2_unpack(f2_fma(c[3], k256, c[2]), e1, o1);
+  uint32_t w = __byte_perm(__float_as_uint(fmaf(o0, 16.f, e0)), __float_as_uint(fmaf(o1, 16.f, e1)),
+                           0x5410);
+  if (!(scale > 1e-30f && scale < 1e30f)) {
     w = 0;
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {
@@ -116,9 +122,13 @@ __device__ __forceinline__ uint32_t kv4_codes8(const float (&x)[8], float scale,
   return w;
 }
 
-__device__ __forceinline__ void kv4_scale_zero(float lo, float hi, float& scale, float& zero) {
-  zero = __bfloat162float(__float2bfloat16_rn(lo));
-  scale = __bfloat162float(__float2bfloat16_rn(__fmul_rn(__fsub_rn(hi, lo), kKv4Inv15)));
+__device__ __forceinline__ float kv4_scale(float lo, float hi) {
+  return __bfloat162float(__float2bfloat16_rn(__fmul_rn(__fsub_rn(hi, lo), kKv4Inv15)));
+}
+__device__ __forceinline__ float kv4_reciprocal(float scale) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(scale));
+  return y;
 }
 
 // Scale, zero and codes of this lane's 8 channels; the group's 8 lanes are
@@ -132,24 +142,26 @@ __device__ __forceinline__ uint32_t kv4_encode8(const float (&x)[8], float& scal
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
   }
-  kv4_scale_zero(lo, hi, scale, zero);
-  return kv4_codes8<false>(x, scale, zero, __frcp_rn(scale));
+  zero = __bfloat162float(__float2bfloat16_rn(lo));
+  scale = kv4_scale(lo, hi);
+  return kv4_codes8<false>(x, scale, zero, kv4_reciprocal(scale));
 }
 // The same for eight bf16 values as they lie in memory (minima and maxima two
 // at a time).
 __device__ __forceinline__ uint32_t kv4_encode8(const uint4& raw, float& scale, float& zero) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t lo = bf16x2_min(bf16x2_min(w[0], w[1]), bf16x2_min(w[2], w[3]));
-  uint32_t hi = bf16x2_max(bf16x2_max(w[0], w[1]), bf16x2_max(w[2], w[3]));
+  const uint32_t lo2 = bf16x2_min(bf16x2_min(w[0], w[1]), bf16x2_min(w[2], w[3]));
+  const uint32_t hi2 = bf16x2_max(bf16x2_max(w[0], w[1]), bf16x2_max(w[2], w[3]));
+  // (minimum, -maximum) in one word from here on
+  uint32_t v = bf16x2_min(__byte_perm(lo2, hi2, 0x5410) ^ 0x80000000u,
+                          __byte_perm(lo2, hi2, 0x7632) ^ 0x80000000u);
 #pragma unroll
-  for (int m = 1; m < 8; m <<= 1) {
-    lo = bf16x2_min(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-    hi = bf16x2_max(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-  }
-  kv4_scale_zero(fminf(bf16_lo(lo), bf16_hi(lo)), fmaxf(bf16_lo(hi), bf16_hi(hi)), scale, zero);
+  for (int m = 1; m < 8; m <<= 1) v = bf16x2_min(v, __shfl_xor_sync(0xffffffffu, v, m));
+  zero = bf16_lo(v);
+  scale = kv4_scale(zero, -bf16_hi(v));
   float x[8];
   Chunk<__nv_bfloat16>::unpack(raw, x);
-  return kv4_codes8<true>(x, scale, zero, __frcp_rn(scale));
+  return kv4_codes8<true>(x, scale, zero, kv4_reciprocal(scale));
 }
 
 // Transpose of an 8 x 8 matrix of nibbles: nibble c of word r <-> nibble r of

@@ -73,20 +73,21 @@ __global__ void __launch_bounds__(256) kv4_quantize_kernel(const T* __restrict__
       if (t < valid) x[p].load(src + static_cast<int64_t>(t) * D);
       else x[p].clear();
     }
+    // token t = r0 + p * TPP = 8h + r of pass p: h = p / HALF, r from the rest
+    constexpr int HALF = PASSES / 2;
+    uint8_t* codes = is_v ? reinterpret_cast<uint8_t*>(&vcode[pair][r0][chunk])
+                          : rec + g * 512 + (r0 * 4 + (x8 >> 1)) * 16 + (x8 & 1) * 4;
+    // (from one pass to the next of a half, and from one half to the other)
+    const int step = is_v ? TPP * static_cast<int>(sizeof(vcode[0][0])) : TPP * 64;
+    const int hop = is_v ? 8 * static_cast<int>(sizeof(vcode[0][0])) : 8;
+    uint8_t* meta = rec + 2 * kv4_code_bytes(D) + (r0 * 2 * NG + g) * 8 + (is_v ? 4 : 0);
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      const int t = r0 + p * TPP;
       float scale, zero;
       const uint32_t w = x[p].encode(scale, zero);
-      if (is_v) {
-        vcode[pair][t][chunk] = w;
-      } else {
-        // word [g][r][c][2h + j]: r = t % 8, c = x8 / 2, h = t / 8, j = x8 % 2
-        *reinterpret_cast<uint32_t*>(
-            rec + g * 512 + ((t & 7) * 4 + (x8 >> 1)) * 16 + ((t >> 3) * 2 + (x8 & 1)) * 4) = w;
-      }
+      *reinterpret_cast<uint32_t*>(codes + (p % HALF) * step + (p / HALF) * hop) = w;
       if (x8 == 0)
-        *reinterpret_cast<uint32_t*>(rec + kv4_meta_at(D, t, g) + (is_v ? 4 : 0)) =
+        *reinterpret_cast<uint32_t*>(meta + (p % HALF) * (TPP * 2 * NG * 8) + (p / HALF) * (NG * 8)) =
             kv4_pack_meta(scale, zero);
     }
     if (is_v) {
