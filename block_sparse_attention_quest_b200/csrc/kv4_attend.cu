@@ -215,6 +215,11 @@ struct Kv4Done {
   int first, parts, late;  // the unit's partials: see kv4_merge
 };
 
+// code - 8 of the low nibbles of both halves, as bf16 numbers (exact)
+__device__ __forceinline__ uint32_t signed_codes(uint32_t w) {
+  return bf16x2_add((w & 0x000f000fu) | 0x43004300u, 0xc308c308u);   // 128 + code, -136
+}
+
 // mma_bf16_16816 with rows 8 .. 15 of the sum left out.
 __device__ __forceinline__ void mma_row0(float& d0, float& d1, const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -247,7 +252,9 @@ __device__ __forceinline__ float ex2_ftz(float x) {
 // times 8 is subtracted at the end, exactly, and zero + 8 * scale takes the
 // place of the zero. (Measured at a 128K context: error against 64 bits 4.8e-3
 // without, 2.4e-3 with it, 1.7e-3 being the output's own rounding.) An fp32
-// call subtracts 8 * p * scale inside the product, so that its sums stay small.
+// call makes bf16 numbers of code - 8 instead, for keys too, so that its sums
+// stay small and of both signs: the tensor cores truncate, and a common sign
+// would add up (outputs over 65000 tokens: 9.9e-6 off, 1.5e-6 with it).
 template <typename T, int D, bool SEL>
 __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     kv4_attend_kernel(Kv4K a) {
@@ -255,12 +262,18 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
   constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;    // bf16 parts of q and of p * scale
   constexpr int NG = D / kKv4Group;
   constexpr int NW = kKv4Warps<T>, ST = kKv4Stages, REC = C::kRec;
-  constexpr float kUp = 18446744073709551616.f;                 // 2^64
+  // the weights' factor, as an exponent and as a number (fp32: none; a sum with
+  // 64 would cost the exponent's argument six bits)
+  constexpr float kOff = PARTS == 1 ? 64.f : 0.f;
+  constexpr float kUp = PARTS == 1 ? 18446744073709551616.f : 1.f;
   constexpr float kDown = 5.9029581035870565e+20f;              // 2^69
   constexpr uint32_t kOnes = 0x00010001u;                       // code 1 in both halves
   constexpr float kMid = 8.f;                                   // code the products are taken about
   constexpr float kMidK = PARTS == 1 ? 0.f : 8.f;
-  constexpr uint32_t kNeg8 = 0x80088008u, kNeg128 = 0x80808080u;   // -8 and, where codes count 16-fold, -8 * 16
+  constexpr float kKeys = PARTS == 1 ? kDown : 1.f;             // what brings q . code back
+  // what brings the running sums back: 2^69 (and 1/16 of it where codes count
+  // 16-fold), for fp32, whose value codes are used as numbers, 2^-64
+  constexpr float kBack = PARTS == 1 ? kDown : 1.f / kUp, kRow8 = PARTS == 1 ? 0.0625f : 1.f;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(8) uint64_t bars[NW][ST];
   __shared__ uint32_t s_total, s_row_start;
@@ -461,25 +474,24 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
             for (int i = 0; i < 8; ++i) sum += f[i];
             float part[8][PARTS];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) bf16_parts<PARTS>(f[i] * kUp, part[i]);
+            for (int i = 0; i < 8; ++i) bf16_parts<PARTS>(f[i], part[i]);
 #pragma unroll
             for (int p = 0; p < PARTS; ++p)
 #pragma unroll
               for (int s = 0; s < 2; ++s) {
                 qb[p][g2 * 4 + 2 * j + s][0] = pack_bf16x2(part[2 * s][p], part[2 * s + 4][p]);
-                qb[p][g2 * 4 + 2 * j + s][1] =
-                    pack_bf16x2(part[2 * s + 1][p] * 0.0625f, part[2 * s + 5][p] * 0.0625f);
+                qb[p][g2 * 4 + 2 * j + s][1] = pack_bf16x2(part[2 * s + 1][p], part[2 * s + 5][p]);
               }
           }
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         // heads 2 cq and 2 cq + 1 of the result layout, in the sums' scale
-        qs0[g2] = __shfl_sync(0xffffffffu, sum, 8 * cq) * (1.f / kDown);
-        qs1[g2] = __shfl_sync(0xffffffffu, sum, 8 * cq + 4) * (1.f / kDown);
+        qs0[g2] = __shfl_sync(0xffffffffu, sum, 8 * cq) * (1.f / kKeys);
+        qs1[g2] = __shfl_sync(0xffffffffu, sum, 8 * cq + 4) * (1.f / kKeys);
       }
     }
-    const float to_log2 = a.scale_log2 * kDown;
+    const float to_log2 = a.scale_log2 * kKeys;
 
     float o[NG * 4][4], ones[NG][2], zo0[NG], zo1[NG];
 #pragma unroll
@@ -489,7 +501,7 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
       ones[i][0] = 0.f; ones[i][1] = 0.f;
       zo0[i] = 0.f; zo1[i] = 0.f;
     }
-    // n = 64 - m with m the reference (log2 units) of the weights 2^(s + n)
+    // n = kOff - m with m the reference (log2 units) of the weights 2^(s + n)
     float n0 = INFINITY, n1 = INFINITY, l0 = 0.f, l1 = 0.f;
 
     for (int k = 0; k < count; ++k) {
@@ -533,21 +545,26 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
           const uint4 kw = *reinterpret_cast<const uint4*>(rec + u * REC + i * 512);
-          // (fp32 takes keys about code kMidK too: smaller sums, smaller errors)
-          float acc[4] = {-kMidK * qs0[i], -kMidK * qs1[i], -kMidK * qs0[i], -kMidK * qs1[i]};
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
           const uint32_t wa[2] = {kw.x, kw.y}, wb[2] = {kw.z, kw.w};
+          // (the small parts of q first: their sums lose least)
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
+          for (int p = PARTS - 1; p >= 0; --p)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t x0 = wa[w] >> (8 * e), x1 = wb[w] >> (8 * e);
-              const uint32_t af[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u,
-                                      x1 & 0x00f000f0u};
+            for (int w = 0; w < 2; ++w)
 #pragma unroll
-              for (int p = 0; p < PARTS; ++p)
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t x0 = wa[w] >> (8 * e), x1 = wb[w] >> (8 * e);
+                uint32_t af[4];
+                if constexpr (PARTS == 1) {
+                  af[0] = x0 & 0x000f000fu; af[1] = x1 & 0x000f000fu;
+                  af[2] = x0 & 0x00f000f0u; af[3] = x1 & 0x00f000f0u;
+                } else {
+                  af[0] = signed_codes(x0); af[1] = signed_codes(x1);
+                  af[2] = signed_codes(x0 >> 4); af[3] = signed_codes(x1 >> 4);
+                }
                 mma_bf16_16816(acc, af, qb[p][i * 4 + 2 * w + e][0], qb[p][i * 4 + 2 * w + e][1]);
-            }
-          }
+              }
           const float ka = bf16_lo(meta[0][i].x), kb = bf16_lo(meta[1][i].x);
           const float za = fmaf(kMidK, ka, bf16_hi(meta[0][i].x));
           const float zb = fmaf(kMidK, kb, bf16_hi(meta[1][i].x));
@@ -590,9 +607,9 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
       const float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
       const float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
       // (n = infinity before the first pair, where the sum is infinite or NaN)
-      if (__any_sync(0xffffffffu, !(x0 + n0 <= 72.f && x1 + n1 <= 72.f))) {
-        const float r0 = fminf(n0, 64.f - warp_max_xor(x0, 16, 4));
-        const float r1 = fminf(n1, 64.f - warp_max_xor(x1, 16, 4));
+      if (__any_sync(0xffffffffu, !(x0 + n0 <= kOff + 8.f && x1 + n1 <= kOff + 8.f))) {
+        const float r0 = fminf(n0, kOff - warp_max_xor(x0, 16, 4));
+        const float r1 = fminf(n1, kOff - warp_max_xor(x1, 16, 4));
         const float al0 = n0 == INFINITY ? 0.f : ex2_ftz(r0 - n0);
         const float al1 = n1 == INFINITY ? 0.f : ex2_ftz(r1 - n1);
         n0 = r0; n1 = r1;
@@ -644,15 +661,20 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const uint32_t x0 = w4[m], x1 = w4[m] >> 8;
-            const uint32_t af[4] = {x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu,
-                                    x1 & 0x00f000f0u};
+            if constexpr (PARTS == 1) {
+              const uint32_t af[4] = {x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu,
+                                      x1 & 0x00f000f0u};
+              mma_bf16_16816(o[i * 4 + m], af, pb[0][0], pb[0][1]);
+            } else {
+              // sixteen tokens at a time, added to the running sums by rounded
+              // additions (the tensor cores' own truncate)
+              const uint32_t af[4] = {signed_codes(x0), signed_codes(x0 >> 4), signed_codes(x1),
+                                      signed_codes(x1 >> 4)};
+              float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-              mma_bf16_16816(o[i * 4 + m], af, pb[p][0], pb[p][1]);
-              if constexpr (PARTS > 1) {
-                const uint32_t mid[4] = {kNeg8, kNeg128, kNeg8, kNeg128};
-                mma_bf16_16816(o[i * 4 + m], mid, pb[p][0], pb[p][1]);
-              }
+              for (int p = PARTS - 1; p >= 0; --p) mma_bf16_16816(y, af, pb[p][0], pb[p][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[i * 4 + m][e] += y[e];
             }
           }
         }
@@ -694,8 +716,8 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     float* sm_l = sm_m + NW * 8;
     const int h0 = 2 * cq, h1 = 2 * cq + 1;
     if (gq == 0) {
-      sm_m[warp * 8 + h0] = 64.f - n0; sm_l[warp * 8 + h0] = l0 * (1.f / kUp);
-      sm_m[warp * 8 + h1] = 64.f - n1; sm_l[warp * 8 + h1] = l1 * (1.f / kUp);
+      sm_m[warp * 8 + h0] = kOff - n0; sm_l[warp * 8 + h0] = l0 * (1.f / kUp);
+      sm_m[warp * 8 + h1] = kOff - n1; sm_l[warp * 8 + h1] = l1 * (1.f / kUp);
     }
     if (h0 < a.G) {
       // rows gq + 8 hold codes read 16 times too large
@@ -703,10 +725,10 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
       for (int i = 0; i < NG * 4; ++i) {
         const int ch = i * 16 + gq;
         const float c0 = kMid * ones[i / 4][0], c1 = kMid * ones[i / 4][1];   // (0 for fp32)
-        sm_o[(warp * 8 + h0) * OR + ch] = fmaf(o[i][0] - c0, kDown, zo0[i / 4]);
-        sm_o[(warp * 8 + h1) * OR + ch] = fmaf(o[i][1] - c1, kDown, zo1[i / 4]);
-        sm_o[(warp * 8 + h0) * OR + ch + 8] = fmaf(fmaf(o[i][2], 0.0625f, -c0), kDown, zo0[i / 4]);
-        sm_o[(warp * 8 + h1) * OR + ch + 8] = fmaf(fmaf(o[i][3], 0.0625f, -c1), kDown, zo1[i / 4]);
+        sm_o[(warp * 8 + h0) * OR + ch] = fmaf(o[i][0] - c0, kBack, zo0[i / 4]);
+        sm_o[(warp * 8 + h1) * OR + ch] = fmaf(o[i][1] - c1, kBack, zo1[i / 4]);
+        sm_o[(warp * 8 + h0) * OR + ch + 8] = fmaf(fmaf(o[i][2], kRow8, -c0), kBack, zo0[i / 4]);
+        sm_o[(warp * 8 + h1) * OR + ch + 8] = fmaf(fmaf(o[i][3], kRow8, -c1), kBack, zo1[i / 4]);
       }
     }
     if (!__syncthreads_and(ok)) {
