@@ -337,6 +337,35 @@ def prefill(q, k_cache, v_cache, desc, length: int, softmax_scale: float, out, w
                              workspace.numel(), _stream(stream)), "resa_prefill")
 
 
+def _tensors(*tensors) -> None:
+    """What the library takes for granted of every tensor."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        at = t.get_device()                       # -1: not a CUDA tensor
+        if at >= 0 and dev is None:
+            dev = torch._C._cuda_getDevice()
+        if at < 0 or at != dev or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous and on the current CUDA device")
+
+
+def _step(q, k_new, v_new, desc, out, lse, lens, B: int, H: int, blocks: int) -> None:
+    """Shapes and types of the arguments of one decode step."""
+    Bq, Hq, d = q.shape
+    if Bq != B or Hq % H or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q and out must be [batch, n_q_heads, head_dim] of one dtype")
+    for t in (k_new, v_new):
+        if t is not None and (t.shape != (B, H, d) or t.dtype != q.dtype):
+            raise ValueError("k_new and v_new must be [batch, n_kv_heads, head_dim] in q's dtype")
+    if desc is not None and (desc.shape != (B, H, blocks, 2, d) or desc.dtype != q.dtype):
+        raise ValueError("desc must be [batch, n_kv_heads, max_len / 16, 2, head_dim] in q's dtype")
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != B * Hq):
+        raise ValueError("lse must be float32 [batch, n_q_heads]")
+    if lens is not None and lens.numel() != B:
+        raise ValueError("lens must be int32 [batch]")
+
+
 def prefill_packed(q, k, v, starts, longest: int, k_cache, v_cache, desc, softmax_scale: float,
                    out, workspace, stream=None) -> None:
     """Causal attention over packed prompts (q, out: [total, Hq, d]; k, v:
@@ -351,6 +380,10 @@ def prefill_packed(q, k, v, starts, longest: int, k_cache, v_cache, desc, softma
         raise ValueError("q, k, v, out and the caches must share a dtype")
     if _lens(starts) is None or starts.numel() != k_cache.shape[0] + 1:
         raise ValueError("starts must be int32 [batch + 1]")
+    if desc is not None and (desc.shape != (*k_cache.shape[:2], k_cache.shape[2] // BLOCK, 2,
+                                            k_cache.shape[3]) or desc.dtype != k_cache.dtype):
+        raise ValueError("desc must be [batch, n_kv_heads, max_len / 16, 2, head_dim]")
+    _tensors(q, k, v, starts, k_cache, v_cache, desc, out, workspace)
     _check(_lib.resa_prefill_packed(
         ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(starts), int(q.shape[0]), int(longest),
         _ptr(k_cache), _ptr(v_cache), _ptr(desc), float(softmax_scale), _ptr(out),
@@ -389,6 +422,12 @@ def decode_dense_weights(q, k_new, v_new, k_cache, v_cache, desc, weights, lengt
     """decode_dense that also adds every token's attention weight to `weights`
     (desc and lse may be None)."""
     dims = dims_for(k_cache, q.shape[1])
+    B, H, L, d = k_cache.shape
+    if v_cache.shape != k_cache.shape or q.shape[2] != d or not (
+            k_cache.dtype == v_cache.dtype == q.dtype):
+        raise ValueError("k_cache and v_cache must be [batch, n_kv_heads, max_len, head_dim] in q's dtype")
+    _step(q, k_new, v_new, desc, out, lse, lens, B, H, L // BLOCK)
+    _tensors(q, k_new, v_new, k_cache, v_cache, desc, weights, out, lse, lens, workspace)
     _check(_lib.resa_decode_dense_weights(
         ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
         _ptr(desc), _weights(weights, k_cache), int(length), _opt_lens(lens),
@@ -409,6 +448,13 @@ def evict(k_cache, v_cache, weights, length: int, budget: int, n_recent: int, k_
         raise ValueError("k_out and v_out must be [batch, n_kv_heads, out_max_len, head_dim]")
     if kept.dtype != torch.int32 or tuple(kept.shape) != (B, H, budget):
         raise ValueError("kept must be int32 [batch, n_kv_heads, budget]")
+    if desc_out is not None and (desc_out.shape != (B, H, Lo // BLOCK, 2, d)
+                                 or desc_out.dtype != k_cache.dtype):
+        raise ValueError("desc_out must be [batch, n_kv_heads, out_max_len / 16, 2, head_dim]")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or (
+            lens is not None and lens.numel() != B):
+        raise ValueError("v_cache must match k_cache, lens must be int32 [batch]")
+    _tensors(k_cache, v_cache, weights, k_out, v_out, desc_out, weights_out, kept, lens, workspace)
     _check(_lib.resa_evict(
         ctypes.byref(dims), _ptr(k_cache), _ptr(v_cache), _weights(weights, k_cache), int(length),
         _opt_lens(lens), int(budget), int(n_recent), Lo, _ptr(k_out), _ptr(v_out), _ptr(desc_out),
@@ -454,18 +500,21 @@ def alloc_kv4_workspace(dims: Dims, length: int, device=None) -> torch.Tensor:
                        device=device or "cuda")
 
 
-def _kv4_rows(k_cache, v_cache, kv4, n_q_heads: int) -> Dims:
+def _kv4_rows(k_cache, v_cache, kv4, n_q_heads: int, lens) -> Dims:
     B, H, L, d = k_cache.shape
     if (kv4.dtype != torch.uint8 or tuple(kv4.shape) != (B, H, L // BLOCK, kv4_record_bytes(d))
             or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype):
         raise ValueError("kv4 must be the uint8 records of k_cache's and v_cache's shape")
+    _tensors(k_cache, v_cache, kv4, lens)
+    if lens is not None and lens.numel() != B:
+        raise ValueError("lens must be int32 [batch]")
     return dims_for(k_cache, n_q_heads)
 
 
 def kv4_quantize(k_cache, v_cache, length: int, kv4, n_q_heads: int, lens=None,
                  stream=None) -> None:
     """The first `length` tokens of every row into 4-bit records."""
-    dims = _kv4_rows(k_cache, v_cache, kv4, n_q_heads)
+    dims = _kv4_rows(k_cache, v_cache, kv4, n_q_heads, lens)
     _check(_lib.resa_kv4_quantize(ctypes.byref(dims), _ptr(k_cache), _ptr(v_cache), int(length),
                                   _opt_lens(lens), _ptr(kv4), _stream(stream)),
            "resa_kv4_quantize")
@@ -474,16 +523,30 @@ def kv4_quantize(k_cache, v_cache, length: int, kv4, n_q_heads: int, lens=None,
 def kv4_dequantize(kv4, length: int, k_cache, v_cache, n_q_heads: int, lens=None,
                    stream=None) -> None:
     """The values the records stand for, into slots [0, length) of the caches."""
-    dims = _kv4_rows(k_cache, v_cache, kv4, n_q_heads)
+    dims = _kv4_rows(k_cache, v_cache, kv4, n_q_heads, lens)
     _check(_lib.resa_kv4_dequantize(ctypes.byref(dims), _ptr(kv4), int(length), _opt_lens(lens),
                                     _ptr(k_cache), _ptr(v_cache), _stream(stream)),
            "resa_kv4_dequantize")
 
 
+def _kv4_step(q, k_new, v_new, kv4, desc, out, lse, lens, workspace) -> Dims:
+    dims = dims_kv4(kv4, q)
+    _step(q, k_new, v_new, desc, out, lse, lens, kv4.shape[0], kv4.shape[1], kv4.shape[2])
+    _tensors(q, k_new, v_new, kv4, desc, out, lse, lens, workspace)
+    return dims
+
+
+def _sel(sel, kv4, n: int) -> None:
+    if sel is not None:
+        _tensors(sel)
+        if sel.dtype != torch.int32 or sel.shape != (kv4.shape[0], kv4.shape[1], n):
+            raise ValueError("sel must be int32 [batch, n_kv_heads, n]")
+
+
 def decode_dense_kv4(q, k_new, v_new, kv4, desc, length: int, softmax_scale: float, out, workspace,
                      lse=None, lens=None, stream=None) -> None:
     """decode_dense on a 4-bit cache (k_new/v_new and desc may be None)."""
-    dims = dims_kv4(kv4, q)
+    dims = _kv4_step(q, k_new, v_new, kv4, desc, out, lse, lens, workspace)
     _check(_lib.resa_decode_dense_kv4(
         ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(kv4), _ptr(desc), int(length),
         _opt_lens(lens), float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace),
@@ -494,7 +557,8 @@ def decode_sparse_kv4(q, k_new, v_new, kv4, desc, length: int, r: float, n_min: 
                       softmax_scale: float, out, workspace, lse=None, sel=None, lens=None,
                       stream=None) -> None:
     """decode_sparse (with lens: decode_sparse_varlen) on a 4-bit cache."""
-    dims = dims_kv4(kv4, q)
+    dims = _kv4_step(q, k_new, v_new, kv4, desc, out, lse, lens, workspace)
+    _sel(sel, kv4, num_selected(length, r, n_min))
     _check(_lib.resa_decode_sparse_kv4(
         ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(kv4), _ptr(desc), int(length),
         _opt_lens(lens), float(r), int(n_min), float(softmax_scale), _ptr(out), _ptr(lse),
@@ -504,7 +568,8 @@ def decode_sparse_kv4(q, k_new, v_new, kv4, desc, length: int, r: float, n_min: 
 def attend_blocks_kv4(q, kv4, length: int, sel, softmax_scale: float, out, workspace, lse=None,
                       stream=None) -> None:
     """attend_blocks on a 4-bit cache."""
-    dims = dims_kv4(kv4, q)
+    dims = _kv4_step(q, None, None, kv4, None, out, lse, None, workspace)
+    _sel(sel, kv4, int(sel.shape[-1]))
     _check(_lib.resa_attend_blocks_kv4(
         ctypes.byref(dims), _ptr(q), _ptr(kv4), int(length), _ptr(sel), int(sel.shape[-1]),
         float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),

@@ -638,10 +638,17 @@ int resa_prefill_packed(const resa_dims* dims, const void* q, const void* k, con
   while (Gt < 8 && s.G % (2 * Gt) == 0) Gt *= 2;
   const int64_t ctas = (total / (128 / Gt) + s.B) * (s.Hq / Gt);
   if (total > 2147483647LL - 512 || ctas > 2147483647LL) return RESA_ERR_UNSUPPORTED;
-  // a CTA reads keys and values of tokens that other CTAs' outputs follow
+  // a CTA reads tokens whose results others write: the outputs are other memory
   const size_t qb = static_cast<size_t>(total) * s.Hq * s.D * 2, kb = qb / s.G;
-  if (overlap(out, qb, q, qb) || overlap(out, qb, k, kb) || overlap(out, qb, v, kb))
-    return RESA_ERR_INVALID_ARG;
+  const size_t cb = static_cast<size_t>(s.B) * s.H * static_cast<size_t>(s.L_max) * s.D * 2;
+  const struct { const void* p; size_t n; } in[3] = {{q, qb}, {k, kb}, {v, kb}},
+      res[4] = {{out, qb}, {k_cache, cb}, {v_cache, cb}, {desc, cb / 8}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 3; ++j)
+      if (overlap(in[j].p, in[j].n, res[i].p, res[i].n)) return RESA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(res[j].p, res[j].n, res[i].p, res[i].n)) return RESA_ERR_INVALID_ARG;
+  }
   PackedArgs r{};
   r.B = s.B; r.T = static_cast<int>(total); r.longest = static_cast<int>(longest < total ? longest : total);
   r.Hq = s.Hq; r.H = s.H; r.G = s.G; r.Gt = Gt; r.D = s.D; r.L_max = s.L_max;
@@ -814,7 +821,7 @@ static int check_kv4_decode(const resa_dims* dims, Shape* s, const void* q, cons
       !aligned16(q) || !aligned16(kv4) || !aligned16(out) || (desc && !aligned16(desc)) ||
       (k_new && (!aligned16(k_new) || !aligned16(v_new))) ||
       (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 || (lens && !lens_ok(lens)) ||
-      len < 1 || !(std::isfinite(softmax_scale) && softmax_scale > 0.f))
+      len < 1 || !(softmax_scale > 0.f && softmax_scale < 1e17f))   // (its product with 2^69 is finite)
     return RESA_ERR_INVALID_ARG;
   if (len > s->L_max) return RESA_ERR_CAPACITY;
   if (workspace_bytes < kv4_layout(*s, len).total) return RESA_ERR_WORKSPACE;

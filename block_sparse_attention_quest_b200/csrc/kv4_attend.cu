@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     // n = kOff - m with m the reference (log2 units) of the weights 2^(s + n)
     float n0 = INFINITY, n1 = INFINITY, l0 = 0.f, l1 = 0.f;
 
-    for (int k = 0; k < count; ++k) {
+    int k = 0;
+    for (; k < count; ++k) {
       const int st = used % ST;
       if (!__all_sync(0xffffffffu, mbar_try_wait(&bars[warp][st], (used / ST) & 1))) {
         const bool arrived = mbar_wait_bounded(&bars[warp][st], (used / ST) & 1, a.ctrl);
@@ -683,10 +684,10 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
       if (k + ST < count) issue(k + ST, st);
     }
     if (!ok) {
-      // wait, within the bound, for this warp's other copies in flight
-      for (int st = 0; st < ST; ++st)
-        if (st != static_cast<int>(used % ST))
-          (void)mbar_wait_bounded(&bars[warp][st], ((used + 1) / ST) & 1, a.ctrl);
+      // wait, within the bound, for this warp's other copies in flight (pairs
+      // k + 1 .. of this piece)
+      for (int i = 1; i < ST && k + i < count; ++i)
+        (void)mbar_wait_bounded(&bars[warp][(used + i) % ST], ((used + i) / ST) & 1, a.ctrl);
       more = false;
     } else {
       more = next_piece(s_done[(piece + 1) & 1]);

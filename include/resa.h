@@ -310,7 +310,8 @@ RESA_API int resa_rectify_varlen(const resa_dims* dims, const void* q_f, const v
  * value should be finite: one that is not reaches every output of its own
  * sequence whose 128-token key tile holds it (also through a masked place),
  * and no other sequence. starts is read on the device only (a captured call
- * can be replayed on other lengths). out must not overlap q, k or v. bf16
+ * can be replayed on other lengths). out, the caches and desc must not overlap
+ * q, k, v or each other (RESA_ERR_INVALID_ARG). bf16
  * only (RESA_ERR_UNSUPPORTED otherwise); any group up to 8. The workspace only
  * carries the error word: resa_workspace_bytes(dims, longest, 0) suffices. */
 RESA_API int resa_prefill_packed(const resa_dims* dims, const void* q, const void* k, const void* v,
@@ -387,7 +388,7 @@ RESA_API int resa_evict(const resa_dims* dims, const void* k_cache, const void* 
  *      scales of token 8h + r, group g: [r][h][g][4].
  *  - Values must be finite and below 2^60 in magnitude, queries below 2^60;
  *    others give unspecified outputs in their own row (NaN and infinity are
- *    not carried through the format).
+ *    not carried through the format). softmax_scale must be below 1e17.
  *  - dims.dtype is the type of q, k, v, desc and out; the records are the same
  *    for both types.
  *  - lens is optional in these calls (NULL: every row has `len` tokens); with
@@ -406,7 +407,8 @@ RESA_API size_t resa_kv4_workspace_bytes(const resa_dims* dims, int64_t len);
 
 /* The first `len` (lens[b]) tokens of every row of k_cache and v_cache into
  * records; slots past a row's end in its last record are zero, later records
- * are not written. */
+ * are not written. (An entry of lens outside [1, len] is clamped; there is no
+ * workspace to flag it in. The same holds for resa_kv4_dequantize.) */
 RESA_API int resa_kv4_quantize(const resa_dims* dims, const void* k_cache, const void* v_cache,
                                int64_t len, const int32_t* lens, void* kv4, void* stream);
 

@@ -384,3 +384,71 @@ def test_offsets_past_32_bits(resa):
     assert resa.workspace_status(ws) == resa.RESA_OK
     check(resa, q, np.broadcast_to(small.cpu().numpy(), (B, H, 17, small.shape[-1])), [n] * B, None,
           out.double().cpu().numpy(), lse.double().cpu().numpy(), 0.09, "bf16", d, H)
+
+
+def test_strided_tensors_are_refused(resa):
+    rec = torch.zeros(1, 2, 4, ops.kv4_record_bytes(64), dtype=torch.uint8, device="cuda")
+    q = torch.zeros(1, 4, 128, dtype=torch.bfloat16, device="cuda")[:, :, :64]
+    ws = resa.alloc_kv4_workspace(resa.dims_kv4(rec, q), 64)
+    with pytest.raises(ValueError):
+        resa.decode_dense_kv4(q, None, None, rec, None, 10, 1.0, torch.zeros_like(q), ws)
+    k = torch.zeros(1, 2, 64, 128, dtype=torch.bfloat16, device="cuda")[:, :, :, ::2]
+    with pytest.raises(ValueError):
+        resa.kv4_quantize(k, k, 64, rec, 4)
+
+
+def test_two_calls_at_once(resa):
+    """Two streams, a workspace each: the results of one call after the other."""
+    args, out = run_dense(resa, 2, 2, 4, 128, "bf16", [3000, 3000], 3008, stale=False)
+    q, _, _, rec, _, n, scale, _, _ = args
+    dims = resa.dims_kv4(rec, q)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(out) for _ in streams]
+    spaces = [resa.alloc_kv4_workspace(dims, n) for _ in streams]
+    lens = torch.tensor([3000, 3000], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, o, ws in zip(streams, outs, spaces):
+            with torch.cuda.stream(st):
+                resa.decode_dense_kv4(q, None, None, rec, None, n, scale, o, ws, lens=lens)
+    torch.cuda.synchronize()
+    for o, ws in zip(outs, spaces):
+        assert torch.equal(o, out) and resa.workspace_status(ws) == resa.RESA_OK
+
+
+def test_a_model_step_from_packed_prompts_to_a_4_bit_cache(resa):
+    """As used together: packed prompts fill the caches and descriptors, the
+    caches become 4-bit records, sparse steps append to them."""
+    B, H, G, d, cap, lens = 3, 2, 4, 128, 512, [300, 17, 451]
+    st = [0, 300, 317, 768]
+    T = st[-1]
+    q, k, v = (rnd(60 + i, T, x, d) for i, x in enumerate((H * G, H, H)))
+    kc = torch.zeros(B, H, cap, d, dtype=torch.bfloat16, device="cuda")
+    vc, desc = torch.zeros_like(kc), torch.zeros(B, H, cap // 16, 2, d, dtype=torch.bfloat16, device="cuda")
+    qt = dev(q, "bf16")
+    out = torch.zeros_like(qt)
+    ws = resa.alloc_workspace(resa.dims_for(kc, H * G), cap)
+    scale = 1.0 / math.sqrt(d)
+    resa.prefill_packed(qt, dev(k, "bf16"), dev(v, "bf16"), torch.tensor(st, dtype=torch.int32, device="cuda"),
+                        451, kc, vc, desc, scale, out, ws)
+    rec = resa.alloc_kv4(B, H, cap, d)
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    resa.kv4_quantize(kc, vc, 451, rec, H * G, lens=lt)
+    dq = torch.zeros(B, H * G, d, dtype=torch.bfloat16, device="cuda")
+    ws4 = resa.alloc_kv4_workspace(resa.dims_kv4(rec, dq), cap)
+    o, lse = torch.zeros_like(dq), torch.zeros(B, H * G, device="cuda")
+    for s in range(20):
+        qs, kn, vn = (rnd(100 + 3 * s + i, B, x, d) for i, x in enumerate((H * G, H, H)))
+        lt += 1
+        n = 451 + s + 1
+        sel = torch.full((B, H, resa.num_selected(n, 0.3, 4)), -5, dtype=torch.int32, device="cuda")
+        resa.decode_sparse_kv4(dev(qs, "bf16"), dev(kn, "bf16"), dev(vn, "bf16"), rec, desc, n, 0.3, 4, scale, o,
+                               ws4, lse=lse, sel=sel, lens=lt)
+    assert resa.workspace_status(ws4) == resa.RESA_OK and resa.workspace_status(ws) == resa.RESA_OK
+    recs, got, gl, ids = rec.cpu().numpy(), o.double().cpu().numpy(), lse.double().cpu().numpy(), sel.cpu().numpy()
+    for b in range(B):
+        for h in range(H):
+            mine = ids[b, h][ids[b, h] >= 0]
+            assert len(mine) == resa.num_selected(int(lt[b]), 0.3, 4) and mine[-1] == (int(lt[b]) - 1) // 16
+            check(resa, qs[b:b + 1, h * G:(h + 1) * G], recs[b:b + 1, h:h + 1], [int(lt[b])], np.array([[mine]]),
+                  got[b:b + 1, h * G:(h + 1) * G], gl[b:b + 1, h * G:(h + 1) * G], scale, "bf16", d, 1)
