@@ -12,6 +12,7 @@ libresa.so is missing. There is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -337,17 +338,31 @@ def prefill(q, k_cache, v_cache, desc, length: int, softmax_scale: float, out, w
                              workspace.numel(), _stream(stream)), "resa_prefill")
 
 
-def _tensors(*tensors) -> None:
-    """What the library takes for granted of every tensor."""
-    dev = None
+def _ptrs(*tensors) -> list:
+    """Addresses of the tensors (None stays None), which have to be contiguous
+    and on the current CUDA device."""
+    out, dev = [], -1
     for t in tensors:
         if t is None:
+            out.append(None)
             continue
         at = t.get_device()                       # -1: not a CUDA tensor
-        if at >= 0 and dev is None:
-            dev = torch._C._cuda_getDevice()
-        if at < 0 or at != dev or not t.is_contiguous():
-            raise ValueError("tensors must be contiguous and on the current CUDA device")
+        if at != dev:
+            if at < 0 or dev >= 0 or at != torch._C._cuda_getDevice():
+                raise ValueError("tensors must be on the current CUDA device")
+            dev = at
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _dims_ref(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype,
+              max_len: int):
+    """Pointer to a Dims of these values, for the library to read."""
+    return ctypes.byref(Dims(batch, n_q_heads, n_kv_heads, head_dim, BLOCK, _dtype_code(dtype),
+                             max_len))
 
 
 def _step(q, k_new, v_new, desc, out, lse, lens, B: int, H: int, blocks: int) -> None:
@@ -362,7 +377,11 @@ def _step(q, k_new, v_new, desc, out, lse, lens, B: int, H: int, blocks: int) ->
         raise ValueError("desc must be [batch, n_kv_heads, max_len / 16, 2, head_dim] in q's dtype")
     if lse is not None and (lse.dtype != torch.float32 or lse.numel() != B * Hq):
         raise ValueError("lse must be float32 [batch, n_q_heads]")
-    if lens is not None and lens.numel() != B:
+    _row_lens(lens, B)
+
+
+def _row_lens(lens, B: int) -> None:
+    if lens is not None and (lens.dtype != torch.int32 or lens.shape != (B,)):
         raise ValueError("lens must be int32 [batch]")
 
 
@@ -371,36 +390,30 @@ def prefill_packed(q, k, v, starts, longest: int, k_cache, v_cache, desc, softma
     """Causal attention over packed prompts (q, out: [total, Hq, d]; k, v:
     [total, Hkv, d]; starts: int32 CUDA tensor [batch + 1]), which also fills
     rows of k_cache and v_cache [batch, Hkv, max_len, d] and desc (or None)."""
-    dims = dims_for(k_cache, q.shape[1])
-    if (tuple(k.shape) != (q.shape[0], k_cache.shape[1], q.shape[2]) or v.shape != k.shape
-            or out.shape != q.shape or k_cache.shape != v_cache.shape
-            or q.shape[2] != k_cache.shape[3]):
+    B, H, L, d = k_cache.shape
+    T, Hq, dq = q.shape
+    if (k.shape != (T, H, d) or v.shape != k.shape or out.shape != q.shape
+            or k_cache.shape != v_cache.shape or dq != d):
         raise ValueError("q, out must be [total, n_q_heads, d] and k, v [total, n_kv_heads, d]")
     if any(t.dtype != k_cache.dtype for t in (q, k, v, v_cache, out)):
         raise ValueError("q, k, v, out and the caches must share a dtype")
-    if _lens(starts) is None or starts.numel() != k_cache.shape[0] + 1:
+    if starts.dtype != torch.int32 or starts.shape != (B + 1,):
         raise ValueError("starts must be int32 [batch + 1]")
-    if desc is not None and (desc.shape != (*k_cache.shape[:2], k_cache.shape[2] // BLOCK, 2,
-                                            k_cache.shape[3]) or desc.dtype != k_cache.dtype):
+    if desc is not None and (desc.shape != (B, H, L // BLOCK, 2, d) or desc.dtype != q.dtype):
         raise ValueError("desc must be [batch, n_kv_heads, max_len / 16, 2, head_dim]")
-    _tensors(q, k, v, starts, k_cache, v_cache, desc, out, workspace)
+    pq, pk, pv, ps, pkc, pvc, pd, po, pw = _ptrs(q, k, v, starts, k_cache, v_cache, desc, out,
+                                                 workspace)
     _check(_lib.resa_prefill_packed(
-        ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(starts), int(q.shape[0]), int(longest),
-        _ptr(k_cache), _ptr(v_cache), _ptr(desc), float(softmax_scale), _ptr(out),
-        _ptr(workspace), workspace.numel(), _stream(stream)), "resa_prefill_packed")
+        _dims_ref(B, Hq, H, d, q.dtype, L), pq, pk, pv, ps, T, int(longest), pkc, pvc, pd,
+        float(softmax_scale), po, pw, workspace.numel(), _stream(stream)), "resa_prefill_packed")
 
 
 # ---- attention weights (float32 [B, H_kv, max_len] running sums) and eviction
 
 
-def _opt_lens(lens):
-    return None if lens is None else _lens(lens)
-
-
-def _weights(weights, k_cache):
-    if weights.dtype != torch.float32 or tuple(weights.shape) != tuple(k_cache.shape[:3]):
+def _weights(weights, B: int, H: int, L: int) -> None:
+    if weights.dtype != torch.float32 or weights.shape != (B, H, L):
         raise ValueError("weights must be float32 [batch, n_kv_heads, max_len]")
-    return _ptr(weights)
 
 
 def weights_workspace_bytes(dims: Dims, length: int) -> int:
@@ -421,18 +434,18 @@ def decode_dense_weights(q, k_new, v_new, k_cache, v_cache, desc, weights, lengt
                          stream=None) -> None:
     """decode_dense that also adds every token's attention weight to `weights`
     (desc and lse may be None)."""
-    dims = dims_for(k_cache, q.shape[1])
     B, H, L, d = k_cache.shape
     if v_cache.shape != k_cache.shape or q.shape[2] != d or not (
             k_cache.dtype == v_cache.dtype == q.dtype):
         raise ValueError("k_cache and v_cache must be [batch, n_kv_heads, max_len, head_dim] in q's dtype")
     _step(q, k_new, v_new, desc, out, lse, lens, B, H, L // BLOCK)
-    _tensors(q, k_new, v_new, k_cache, v_cache, desc, weights, out, lse, lens, workspace)
+    _weights(weights, B, H, L)
+    pq, pkn, pvn, pk, pv, pd, pwt, po, pl, pn, pw = _ptrs(
+        q, k_new, v_new, k_cache, v_cache, desc, weights, out, lse, lens, workspace)
     _check(_lib.resa_decode_dense_weights(
-        ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
-        _ptr(desc), _weights(weights, k_cache), int(length), _opt_lens(lens),
-        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
-        _stream(stream)), "resa_decode_dense_weights")
+        _dims_ref(B, q.shape[1], H, d, q.dtype, L), pq, pkn, pvn, pk, pv, pd, pwt, int(length), pn,
+        float(softmax_scale), po, pl, pw, workspace.numel(), _stream(stream)),
+        "resa_decode_dense_weights")
 
 
 def evict(k_cache, v_cache, weights, length: int, budget: int, n_recent: int, k_out, v_out,
@@ -440,26 +453,26 @@ def evict(k_cache, v_cache, weights, length: int, budget: int, n_recent: int, k_
     """Cut every (row, KV head) to its newest n_recent tokens and the
     budget - n_recent others of the largest weight (desc_out and weights_out
     may be None; kept: int32 [B, H_kv, budget])."""
-    dims = dims_for(k_cache, n_q_heads)
-    B, H, Lo, d = k_out.shape
-    if (tuple(k_out.shape) != (k_cache.shape[0], k_cache.shape[1], Lo, k_cache.shape[3])
-            or v_out.shape != k_out.shape or k_out.dtype != k_cache.dtype
-            or v_out.dtype != k_cache.dtype):
-        raise ValueError("k_out and v_out must be [batch, n_kv_heads, out_max_len, head_dim]")
-    if kept.dtype != torch.int32 or tuple(kept.shape) != (B, H, budget):
-        raise ValueError("kept must be int32 [batch, n_kv_heads, budget]")
+    B, H, L, d = k_cache.shape
+    Lo = k_out.shape[2]
+    if not (k_out.shape == v_out.shape == (B, H, Lo, d) and v_cache.shape == k_cache.shape
+            and k_cache.dtype == v_cache.dtype == k_out.dtype == v_out.dtype):
+        raise ValueError("the caches must be [batch, n_kv_heads, max_len, head_dim] of one dtype")
+    _weights(weights, B, H, L)
+    if weights_out is not None:
+        _weights(weights_out, B, H, Lo)
     if desc_out is not None and (desc_out.shape != (B, H, Lo // BLOCK, 2, d)
                                  or desc_out.dtype != k_cache.dtype):
         raise ValueError("desc_out must be [batch, n_kv_heads, out_max_len / 16, 2, head_dim]")
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or (
-            lens is not None and lens.numel() != B):
-        raise ValueError("v_cache must match k_cache, lens must be int32 [batch]")
-    _tensors(k_cache, v_cache, weights, k_out, v_out, desc_out, weights_out, kept, lens, workspace)
+    if kept.dtype != torch.int32 or kept.shape != (B, H, budget):
+        raise ValueError("kept must be int32 [batch, n_kv_heads, budget]")
+    _row_lens(lens, B)
+    pk, pv, pwt, pko, pvo, pdo, pwo, pi, pn, pw = _ptrs(
+        k_cache, v_cache, weights, k_out, v_out, desc_out, weights_out, kept, lens, workspace)
     _check(_lib.resa_evict(
-        ctypes.byref(dims), _ptr(k_cache), _ptr(v_cache), _weights(weights, k_cache), int(length),
-        _opt_lens(lens), int(budget), int(n_recent), Lo, _ptr(k_out), _ptr(v_out), _ptr(desc_out),
-        None if weights_out is None else _weights(weights_out, k_out), _ptr(kept),
-        _ptr(workspace), workspace.numel(), _stream(stream)), "resa_evict")
+        _dims_ref(B, int(n_q_heads), H, d, k_cache.dtype, L), pk, pv, pwt, int(length), pn,
+        int(budget), int(n_recent), Lo, pko, pvo, pdo, pwo, pi, pw, workspace.numel(),
+        _stream(stream)), "resa_evict")
 
 
 # ---- the cache in 4 bits: a uint8 tensor [B, H_kv, max_len / 16, record] of
@@ -500,56 +513,57 @@ def alloc_kv4_workspace(dims: Dims, length: int, device=None) -> torch.Tensor:
                        device=device or "cuda")
 
 
-def _kv4_rows(k_cache, v_cache, kv4, n_q_heads: int, lens) -> Dims:
+def _kv4_rows(k_cache, v_cache, kv4, n_q_heads: int, lens):
+    """Dims and addresses (k, v, kv4, lens) of a call on whole rows."""
     B, H, L, d = k_cache.shape
-    if (kv4.dtype != torch.uint8 or tuple(kv4.shape) != (B, H, L // BLOCK, kv4_record_bytes(d))
+    if (kv4.dtype != torch.uint8 or kv4.shape != (B, H, L // BLOCK, kv4_record_bytes(d))
             or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype):
         raise ValueError("kv4 must be the uint8 records of k_cache's and v_cache's shape")
-    _tensors(k_cache, v_cache, kv4, lens)
-    if lens is not None and lens.numel() != B:
-        raise ValueError("lens must be int32 [batch]")
-    return dims_for(k_cache, n_q_heads)
+    _row_lens(lens, B)
+    return (_dims_ref(B, int(n_q_heads), H, d, k_cache.dtype, L),
+            *_ptrs(k_cache, v_cache, kv4, lens))
 
 
 def kv4_quantize(k_cache, v_cache, length: int, kv4, n_q_heads: int, lens=None,
                  stream=None) -> None:
     """The first `length` tokens of every row into 4-bit records."""
-    dims = _kv4_rows(k_cache, v_cache, kv4, n_q_heads, lens)
-    _check(_lib.resa_kv4_quantize(ctypes.byref(dims), _ptr(k_cache), _ptr(v_cache), int(length),
-                                  _opt_lens(lens), _ptr(kv4), _stream(stream)),
+    dims, pk, pv, p4, pn = _kv4_rows(k_cache, v_cache, kv4, n_q_heads, lens)
+    _check(_lib.resa_kv4_quantize(dims, pk, pv, int(length), pn, p4, _stream(stream)),
            "resa_kv4_quantize")
 
 
 def kv4_dequantize(kv4, length: int, k_cache, v_cache, n_q_heads: int, lens=None,
                    stream=None) -> None:
     """The values the records stand for, into slots [0, length) of the caches."""
-    dims = _kv4_rows(k_cache, v_cache, kv4, n_q_heads, lens)
-    _check(_lib.resa_kv4_dequantize(ctypes.byref(dims), _ptr(kv4), int(length), _opt_lens(lens),
-                                    _ptr(k_cache), _ptr(v_cache), _stream(stream)),
+    dims, pk, pv, p4, pn = _kv4_rows(k_cache, v_cache, kv4, n_q_heads, lens)
+    _check(_lib.resa_kv4_dequantize(dims, p4, int(length), pn, pk, pv, _stream(stream)),
            "resa_kv4_dequantize")
 
 
-def _kv4_step(q, k_new, v_new, kv4, desc, out, lse, lens, workspace) -> Dims:
-    dims = dims_kv4(kv4, q)
-    _step(q, k_new, v_new, desc, out, lse, lens, kv4.shape[0], kv4.shape[1], kv4.shape[2])
-    _tensors(q, k_new, v_new, kv4, desc, out, lse, lens, workspace)
-    return dims
+def _kv4_step(q, k_new, v_new, kv4, desc, out, lse, lens, sel, workspace):
+    """Dims and addresses of a decode call on a 4-bit cache."""
+    B, H, M, rec = kv4.shape
+    d = q.shape[-1]
+    if kv4.dtype != torch.uint8 or rec != BLOCK * (d + 8 * (d // 64)):
+        raise ValueError(f"kv4 must be uint8 records of {kv4_record_bytes(d)} bytes")
+    _step(q, k_new, v_new, desc, out, lse, lens, B, H, M)
+    return (_dims_ref(B, q.shape[1], H, d, q.dtype, M * BLOCK),
+            *_ptrs(q, k_new, v_new, kv4, desc, out, lse, lens, sel, workspace))
 
 
 def _sel(sel, kv4, n: int) -> None:
-    if sel is not None:
-        _tensors(sel)
-        if sel.dtype != torch.int32 or sel.shape != (kv4.shape[0], kv4.shape[1], n):
-            raise ValueError("sel must be int32 [batch, n_kv_heads, n]")
+    if sel is not None and (sel.dtype != torch.int32
+                            or sel.shape != (kv4.shape[0], kv4.shape[1], n)):
+        raise ValueError("sel must be int32 [batch, n_kv_heads, n]")
 
 
 def decode_dense_kv4(q, k_new, v_new, kv4, desc, length: int, softmax_scale: float, out, workspace,
                      lse=None, lens=None, stream=None) -> None:
     """decode_dense on a 4-bit cache (k_new/v_new and desc may be None)."""
-    dims = _kv4_step(q, k_new, v_new, kv4, desc, out, lse, lens, workspace)
+    dims, pq, pkn, pvn, p4, pd, po, pl, pn, _, pw = _kv4_step(q, k_new, v_new, kv4, desc, out, lse,
+                                                              lens, None, workspace)
     _check(_lib.resa_decode_dense_kv4(
-        ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(kv4), _ptr(desc), int(length),
-        _opt_lens(lens), float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace),
+        dims, pq, pkn, pvn, p4, pd, int(length), pn, float(softmax_scale), po, pl, pw,
         workspace.numel(), _stream(stream)), "resa_decode_dense_kv4")
 
 
@@ -557,23 +571,24 @@ def decode_sparse_kv4(q, k_new, v_new, kv4, desc, length: int, r: float, n_min: 
                       softmax_scale: float, out, workspace, lse=None, sel=None, lens=None,
                       stream=None) -> None:
     """decode_sparse (with lens: decode_sparse_varlen) on a 4-bit cache."""
-    dims = _kv4_step(q, k_new, v_new, kv4, desc, out, lse, lens, workspace)
     _sel(sel, kv4, num_selected(length, r, n_min))
+    dims, pq, pkn, pvn, p4, pd, po, pl, pn, ps, pw = _kv4_step(q, k_new, v_new, kv4, desc, out, lse,
+                                                               lens, sel, workspace)
     _check(_lib.resa_decode_sparse_kv4(
-        ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(kv4), _ptr(desc), int(length),
-        _opt_lens(lens), float(r), int(n_min), float(softmax_scale), _ptr(out), _ptr(lse),
-        _ptr(sel), _ptr(workspace), workspace.numel(), _stream(stream)), "resa_decode_sparse_kv4")
+        dims, pq, pkn, pvn, p4, pd, int(length), pn, float(r), int(n_min), float(softmax_scale),
+        po, pl, ps, pw, workspace.numel(), _stream(stream)), "resa_decode_sparse_kv4")
 
 
 def attend_blocks_kv4(q, kv4, length: int, sel, softmax_scale: float, out, workspace, lse=None,
                       stream=None) -> None:
     """attend_blocks on a 4-bit cache."""
-    dims = _kv4_step(q, None, None, kv4, None, out, lse, None, workspace)
-    _sel(sel, kv4, int(sel.shape[-1]))
-    _check(_lib.resa_attend_blocks_kv4(
-        ctypes.byref(dims), _ptr(q), _ptr(kv4), int(length), _ptr(sel), int(sel.shape[-1]),
-        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
-        _stream(stream)), "resa_attend_blocks_kv4")
+    n = int(sel.shape[-1])
+    _sel(sel, kv4, n)
+    dims, pq, _, _, p4, _, po, pl, _, ps, pw = _kv4_step(q, None, None, kv4, None, out, lse, None,
+                                                         sel, workspace)
+    _check(_lib.resa_attend_blocks_kv4(dims, pq, p4, int(length), ps, n, float(softmax_scale), po,
+                                       pl, pw, workspace.numel(), _stream(stream)),
+           "resa_attend_blocks_kv4")
 
 
 def wait_check(flag, target: int, limit_us: int, workspace, stream=None) -> None:
