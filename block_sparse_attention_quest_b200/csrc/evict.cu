@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* _
   __shared__ uint32_t warp_tot[kEvWarps];
   __shared__ uint32_t tab[U][kEvWarps];           // per (u, warp): keys above | equal << 16
   __shared__ uint32_t s_prefix, s_remaining, s_whole;
-  __shared__ uint32_t s_count[2];                 // keys above, equal to the threshold
+  __shared__ __align__(8) uint32_t s_count[2];    // keys above, equal to the threshold
   cg::cluster_group cluster = cg::this_cluster();
   auto all_sync = [&] {
     if constexpr (CL > 1) cluster.sync();
@@ -283,6 +283,22 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* _
     return inc - mine;
   };
   uint32_t base_gt = 0, base_eq = 0;              // of this CTA, then running
+  // adds the counts of the cluster's earlier CTAs; the barrier that keeps any
+  // CTA from leaving while another reads it is waited for at the very end
+  auto earlier_ctas = [&] {
+    if constexpr (CL > 1) {
+      uint2 c[CL];
+#pragma unroll
+      for (int i = 0; i < CL; ++i)
+        c[i] = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(s_count, i));
+#pragma unroll
+      for (int i = 0; i < CL; ++i) {
+        base_gt += i < rank ? c[i].x : 0u;
+        base_eq += i < rank ? c[i].y : 0u;
+      }
+      cluster.barrier_arrive();
+    }
+  };
   auto place = [&](int u, int at, uint32_t off, uint32_t gt, uint32_t eq) {
     // off: counts before this thread's four keys, within the CTA
     uint32_t g_at = base_gt + (off & 0xffffu), e_at = base_eq + (off >> 16);
@@ -323,17 +339,8 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* _
       }
       if (lane == 0) { s_count[0] = run & 0xffffu; s_count[1] = run >> 16; }
     }
-    if constexpr (CL > 1) {
-      cluster.sync();
-      for (int i = 0; i < rank; ++i) {
-        const uint32_t* other = cluster.map_shared_rank(s_count, i);
-        base_gt += other[0];
-        base_eq += other[1];
-      }
-      cluster.sync();                             // no CTA leaves while another reads it
-    } else {
-      __syncthreads();
-    }
+    all_sync();
+    earlier_ctas();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       uint32_t gt, eq;
@@ -355,14 +362,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* _
     (void)ev_scan(n_eq, warp_tot, t_eq);
     if (tid == 0) { s_count[0] = t_gt; s_count[1] = t_eq; }
     all_sync();
-    if constexpr (CL > 1) {
-      for (int i = 0; i < rank; ++i) {
-        const uint32_t* other = cluster.map_shared_rank(s_count, i);
-        base_gt += other[0];
-        base_eq += other[1];
-      }
-      cluster.sync();
-    }
+    earlier_ctas();
     for (int u = 0; u < rounds; ++u) {
       uint32_t gt, eq, all;
       load(u, 0);
@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* _
       base_eq += all >> 16;
     }
   }
+  if constexpr (CL > 1) cluster.barrier_wait();
 }
 
 // ---------------------------------------------------------------------- gather
