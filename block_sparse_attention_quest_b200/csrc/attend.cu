@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(NW * 32) attend_bf16_kernel(const __grid_const
 }
 
 // ---------------------------------------------------------------------- fp32
-template <int D, int NW, bool KEEP = false>
+template <int D, int NW>
 __global__ void __launch_bounds__(NW * 32) attend_f32_kernel(AttnK a) {
   constexpr int P = D + 1;                    // padded row (conflict-free column reads)
   constexpr int CPL = D / 32;                 // output channels per lane
@@ -231,11 +231,6 @@ __global__ void __launch_bounds__(NW * 32) attend_f32_kernel(AttnK a) {
           part = fmaf(sq[h * D + c], Ks[t * P + c], part);
         part += __shfl_xor_sync(0xffffffffu, part, 16);
         const float z = valid ? part * a.scale_log2 : -INFINITY;
-        if constexpr (KEEP) {
-          if (valid && half == 0)
-            a.logits[((static_cast<int64_t>(b) * a.H + g) * a.logit_stride +
-                      static_cast<int64_t>(j) * kBlock + t) * a.G + h] = z;
-        }
         float mx = z;
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -274,7 +269,177 @@ __global__ void __launch_bounds__(NW * 32) attend_f32_kernel(AttnK a) {
     }
   }
   __syncthreads();
-  cta_finish<float, D, NW, KEEP>(a, sm, br, g, s_idx);
+  cta_finish<float, D, NW>(a, sm, br, g, s_idx);
+}
+
+// The weight-keeping fp32 step (every block, one query row). fp32 products on
+// CUDA cores as above, but bound by HBM: each warp keeps three half tiles (K
+// or V of 16 tokens) in shared memory, two of them on their way while it works
+// on the third (asynchronous copies; rows D + 4 floats apart, so that 16-byte
+// reads of one column group by consecutive tokens hit all banks), every K and
+// V value is read from shared memory once for all heads of the group, and the
+// reference maximum moves only when a logit exceeds it by 2^8.
+template <int D, int NW>
+struct KeepF32Cfg {
+  static constexpr int kRow = D + 4;
+  static constexpr int kHalf = kBlock * kRow;                    // floats of a half tile
+  static constexpr int kSmem = (8 * D + NW * 3 * kHalf) * 4;
+  static_assert(merge_floats(D, NW) <= NW * 3 * kHalf, "merge area");
+};
+
+template <int D, int NW>
+__global__ void __launch_bounds__(NW * 32) attend_f32_keep_kernel(AttnK a) {
+  using C = KeepF32Cfg<D, NW>;
+  constexpr int CPL = D / 32;                     // output channels per lane, consecutive
+  extern __shared__ __align__(16) float smk[];
+  float* sq = smk;                                // [8][D]
+  const int s_idx = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* tiles = smk + 8 * D + warp * 3 * C::kHalf;
+  grid_dependency_wait();
+  const int64_t len_r = query_len(a, b, 0);
+  int i0, i1;
+  split_range(a, s_idx, len_r, i0, i1);
+  const int count = i1 - i0 > warp ? (i1 - i0 - warp + NW - 1) / NW : 0;
+  const int64_t bh = static_cast<int64_t>(b) * a.H + g;
+  const float* kc = static_cast<const float*>(a.k) + bh * a.L_max * D;
+  const float* vc = static_cast<const float*>(a.v) + bh * a.L_max * D;
+  // half tile n of this warp: K (even n) or V of its block n / 2; slots past
+  // the end of the row arrive as zeros
+  auto issue = [&](int n) {
+    const int k = n >> 1;
+    if (k < count) {
+      const int64_t t0 = static_cast<int64_t>(i0 + warp + k * NW) * kBlock;
+      const float* src = (n & 1 ? vc : kc) + t0 * D;
+      float* dst = tiles + (n % 3) * C::kHalf;
+#pragma unroll 4
+      for (int e = lane; e < kBlock * D / 4; e += 32) {
+        const int row = e / (D / 4), c = (e % (D / 4)) * 4;
+        const bool in = t0 + row < len_r;
+        cp_async16_zfill(dst + row * C::kRow + c, in ? src + row * D + c : src, in ? 16u : 0u);
+      }
+    }
+    cp_async_commit();                            // (an empty group past the last)
+  };
+  issue(0);
+  issue(1);
+  issue(2);
+  const float* qg = static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.Hq + g * a.G) * D;
+  for (int i = threadIdx.x; i < a.G * D; i += NW * 32) sq[i] = qg[i];
+  __syncthreads();
+
+  const int t = lane & 15, half = lane >> 4;
+  float m[8], l[8], acc[8][CPL];
+#pragma unroll
+  for (int h = 0; h < 8; ++h) {
+    m[h] = -INFINITY;
+    l[h] = 0.f;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) acc[h][i] = 0.f;
+  }
+#pragma unroll 1
+  for (int k = 0; k < count; ++k) {
+    const int j = i0 + warp + k * NW;
+    // ---- logits of token t (both halves of the channels, summed by a shuffle)
+    cp_async_wait<2>();
+    __syncwarp();
+    float z[8];
+    {
+      const float* kr = tiles + ((2 * k) % 3) * C::kHalf + t * C::kRow + half * (D / 2);
+      const float* qr = sq + half * (D / 2);
+#pragma unroll
+      for (int h = 0; h < 8; ++h) z[h] = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < D / 2; c += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(kr + c);
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+          if (h < a.G) {
+            const float4 y = *reinterpret_cast<const float4*>(qr + h * D + c);
+            z[h] = fmaf(y.x, x.x, z[h]);
+            z[h] = fmaf(y.y, x.y, z[h]);
+            z[h] = fmaf(y.z, x.z, z[h]);
+            z[h] = fmaf(y.w, x.w, z[h]);
+          }
+      }
+    }
+    __syncwarp();                                 // the K slot is read
+    issue(2 * k + 3);
+    const int64_t tok = static_cast<int64_t>(j) * kBlock + t;
+    const bool valid = tok < len_r;
+    float* keep = a.logits + (bh * a.logit_stride + tok) * a.G;
+    bool grow = false;
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h < a.G) {
+        z[h] += __shfl_xor_sync(0xffffffffu, z[h], 16);
+        z[h] = valid ? z[h] * a.scale_log2 : -INFINITY;
+        if (valid && half == 0) keep[h] = z[h];
+        grow |= !(z[h] <= m[h] + 8.f);
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        if (h < a.G) {
+          const float mn = fmaxf(m[h], warp_max_xor(z[h], 8, 1));
+          const float al = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
+          m[h] = mn;
+          l[h] *= al;
+#pragma unroll
+          for (int i = 0; i < CPL; ++i) acc[h][i] *= al;
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h < a.G) {
+        z[h] = exp2f(z[h] - m[h]);                // the weight from here on
+        l[h] += z[h];
+      }
+    // ---- values: lane's channels CPL * lane ..
+    cp_async_wait<2>();
+    __syncwarp();
+    const float* vr = tiles + ((2 * k + 1) % 3) * C::kHalf + lane * CPL;
+#pragma unroll 4
+    for (int tt = 0; tt < kBlock; ++tt) {
+      float x[CPL];
+      if constexpr (CPL == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(vr + tt * C::kRow);
+        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(vr + tt * C::kRow);
+        x[0] = y.x; x[1] = y.y;
+      }
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        if (h < a.G) {
+          const float p = __shfl_sync(0xffffffffu, z[h], tt);
+#pragma unroll
+          for (int i = 0; i < CPL; ++i) acc[h][i] = fmaf(p, x[i], acc[h][i]);
+        }
+    }
+    __syncwarp();                                 // the V slot is read
+    issue(2 * k + 4);
+  }
+  cp_async_wait<0>();
+  grid_launch_dependents();
+  __syncthreads();
+  float* sm = smk + 8 * D;                        // reuse: needs merge_floats(D, NW) floats
+  constexpr int OR = merge_row(D);
+  float* sm_o = sm;
+  float* sm_m = sm + NW * 8 * OR;
+  float* sm_l = sm_m + NW * 8;
+#pragma unroll
+  for (int h = 0; h < 8; ++h) {
+    if (h < a.G) {
+#pragma unroll
+      for (int o = 8; o >= 1; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+      if (lane == 0) { sm_m[warp * 8 + h] = m[h]; sm_l[warp * 8 + h] = l[h]; }
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) sm_o[(warp * 8 + h) * OR + lane * CPL + i] = acc[h][i];
+    }
+  }
+  __syncthreads();
+  cta_finish<float, D, NW, true>(a, sm, b, g, s_idx);
 }
 
 // ---------------------------------------------------------------------- launch
@@ -307,7 +472,7 @@ static cudaError_t attend_bf16_t(const Shape& s, const AttnK& k, const AttnArgs&
   return cudaLaunchKernelEx(&cfg, attend_bf16_kernel<D, kNW, kStages, KEEP>, *a.tm_k, *a.tm_v, k);
 }
 
-template <int D, bool KEEP>
+template <int D>
 static cudaError_t attend_f32_t(const Shape& s, const AttnK& k, const AttnArgs& a,
                                 cudaStream_t st) {
   const size_t tiles = static_cast<size_t>(kNW) * 2 * 16 * (D + 1);
@@ -317,7 +482,7 @@ static cudaError_t attend_f32_t(const Shape& s, const AttnK& k, const AttnArgs& 
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<D, kNW, KEEP>,
+    cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<D, kNW>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -333,7 +498,33 @@ static cudaError_t attend_f32_t(const Shape& s, const AttnK& k, const AttnArgs& 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attend_f32_kernel<D, kNW, KEEP>, k);
+  return cudaLaunchKernelEx(&cfg, attend_f32_kernel<D, kNW>, k);
+}
+
+template <int D>
+static cudaError_t attend_f32_keep_t(const Shape& s, const AttnK& k, const AttnArgs& a,
+                                     cudaStream_t st) {
+  using C = KeepF32Cfg<D, kNW>;
+  static std::atomic<bool> attr_set[64];   // per device; launches may come from several host threads
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(attend_f32_keep_kernel<D, kNW>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.S, s.H, s.B);
+  cfg.blockDim = dim3(kNW * 32);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attend_f32_keep_kernel<D, kNW>, k);
 }
 
 int attend_ctas_per_sm(const Shape& s) { return s.bf16 ? 1 : 2; }
@@ -350,11 +541,11 @@ cudaError_t launch_attend(const Shape& s, const AttnArgs& a, cudaStream_t st) {
   if (a.logits != nullptr) {
     if (s.bf16)
       return s.D == 128 ? attend_bf16_t<128, true>(s, k, a, st) : attend_bf16_t<64, true>(s, k, a, st);
-    return s.D == 128 ? attend_f32_t<128, true>(s, k, a, st) : attend_f32_t<64, true>(s, k, a, st);
+    return s.D == 128 ? attend_f32_keep_t<128>(s, k, a, st) : attend_f32_keep_t<64>(s, k, a, st);
   }
   if (s.bf16)
     return s.D == 128 ? attend_bf16_t<128, false>(s, k, a, st) : attend_bf16_t<64, false>(s, k, a, st);
-  return s.D == 128 ? attend_f32_t<128, false>(s, k, a, st) : attend_f32_t<64, false>(s, k, a, st);
+  return s.D == 128 ? attend_f32_t<128>(s, k, a, st) : attend_f32_t<64>(s, k, a, st);
 }
 
 }  // namespace resa

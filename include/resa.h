@@ -332,8 +332,8 @@ RESA_API int resa_prefill_packed(const resa_dims* dims, const void* q, const voi
  * invalid dims or len < 1. */
 RESA_API size_t resa_weights_workspace_bytes(const resa_dims* dims, int64_t len);
 
-/* resa_decode_dense (same arguments, same out and lse) that also adds each
- * token's attention weight, summed over the group's query heads,
+/* resa_decode_dense (same arguments; in bf16 the same out and lse bit for bit)
+ * that also adds each token's attention weight, summed over the group's query heads,
  *     weights[b][g][t] += sum_{h in group g} exp(scale * q_h . k_t - lse_h),
  * for t < len (lens[b]). With k_new the newest token's sum starts at this step
  * (its slot is set, whatever it held); other slots keep adding up. Slots at or

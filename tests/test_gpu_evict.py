@@ -74,9 +74,25 @@ def test_weights_of_a_step(resa, dtype, d, G, lens, ragged):
         resa.decode_dense_varlen(qt, knt, vnt, k2, v2, d2, lt, n, scale, o2, ws2, lse=l2)
     else:
         resa.decode_dense(qt, knt, vnt, k2, v2, d2, n, scale, o2, ws2, lse=l2)
-    assert torch.equal(out, o2) and torch.equal(lse, l2) and torch.equal(desc, d2)
+    assert torch.equal(kt.nan_to_num(), k2.nan_to_num()) and torch.equal(vt.nan_to_num(), v2.nan_to_num())
+    assert torch.equal(desc, d2)
     got = wt.cpu().numpy()
     kf, vf = k2.double().cpu().numpy(), v2.double().cpu().numpy()
+    if dtype == "bf16":
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+    else:
+        # (a kernel of its own in fp32) sums of d products and of n weighted
+        # values, each term rounded once: n 2^-24 of the magnitudes at worst
+        on, ln = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        for b, x in enumerate(lens):
+            for h in range(H):
+                qs = q[b, h * G:(h + 1) * G].astype(np.float64)
+                o, e, w = ops.attend_row(qs, kf[b, h, :x], vf[b, h, :x], scale)
+                for i in range(G):
+                    rel = weight_bounds(qs[i], kf[b, h, :x], w[i], scale)
+                    mags = w[i] @ np.abs(vf[b, h, :x])
+                    assert (np.abs(on[b, h * G + i] - o[i]) <= (rel + (x + 64) * 2.0 ** -24) * mags + 1e-37).all()
+                    assert abs(ln[b, h * G + i] - e[i]) <= rel + (x + 64) * 2.0 ** -24 + 2.0 ** -22 * abs(e[i])
 
     def one_step(prev, fresh):
         want, tol = prev.astype(np.float64), np.zeros(prev.shape)
@@ -98,7 +114,7 @@ def test_weights_of_a_step(resa, dtype, d, G, lens, ragged):
     assert resa.workspace_status(ws) == resa.RESA_OK
     want, tol = one_step(got, False)
     assert (np.abs(wt.cpu().numpy() - want) <= tol).all()
-    assert torch.equal(out, o2)
+    assert dtype == "f32" or torch.equal(out, o2)
 
 
 # --------------------------------------------------------------------- eviction
