@@ -247,7 +247,11 @@ int run_attention(const Shape& s, const void* q, int R, int64_t len0, const int3
                   const int32_t* windows = nullptr, float* logits = nullptr,
                   float* ml = nullptr) {
   const int64_t min_blocks = sel ? n_sel : blocks_of(len0);
-  const int S = splits_for(s.B * s.H * R, min_blocks, num_sms, s);
+  int S = splits_for(s.B * s.H * R, min_blocks, num_sms, s);
+  // the weight-keeping fp32 kernel's tiles leave room for one CTA per SM at
+  // head_dim 128: more splits than that would run as a second wave
+  if (logits != nullptr && !s.bf16 && s.D == 128 && S > num_sms / (s.B * s.H))
+    S = num_sms / (s.B * s.H) > 1 ? num_sms / (s.B * s.H) : 1;
   AttnArgs a{};
   a.q = q; a.R = R; a.len0 = len0; a.sel = sel; a.n_sel = n_sel; a.S = S; a.scale = scale;
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
