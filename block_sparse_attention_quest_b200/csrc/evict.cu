@@ -7,7 +7,8 @@
 //   w_t += sum_h 2^(logit_ht - m_h) / l_h
 // follow in a kernel of their own, because no weight is known before the last
 // split has been merged. Reading the logits back (4 bytes per head and token,
-// from L2) replaces a second pass over the keys (2 d bytes per token).
+// from L2) replaces a second pass over the keys (2 d bytes per token). A 128K
+// step of 32/8 heads takes 99.5 us: append 3.5, attention 86, sums about 10.
 //
 // Eviction keeps, per (row, KV head), the newest `recent` tokens and of the
 // others the budget - recent with the largest sums, in their order.
@@ -147,7 +148,9 @@ __device__ __forceinline__ uint32_t ev_scan(uint32_t x, uint32_t* warp_tot, uint
 // which the threshold bin is taken whole is the last one. Then the keys above
 // and those equal to the threshold are counted per (u, warp); one scan over
 // those counts and the CTAs' totals gives every kept token its place in the
-// list. Latency-bound: a barrier and a round of remote reads per pass.
+// list. Latency-bound: 23 us for 8 heads of 128K weights, of which 4.5 per pass
+// (1.1 counting, 2.8 barrier and remote reads, 0.6 the decision); one CTA of
+// 4K weights 8 us.
 template <int CL, int KPT>
 __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* __restrict__ weights,
                                                                   int32_t* __restrict__ kept, int H,
@@ -378,7 +381,9 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const float* _
 
 // ---------------------------------------------------------------------- gather
 // One warp per 16-token block of the new cache: its rows are copied from where
-// `kept` says, their minimum and maximum become the block's descriptor.
+// `kept` says, their minimum and maximum become the block's descriptor. 21 us
+// for 16384 of 128K tokens of 8 heads, d = 128 (134 MB read and written, rows
+// of 256 bytes scattered).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) evict_gather_kernel(EvictArgs a, int H, int64_t L_max,
                                                            int M, int64_t total) {

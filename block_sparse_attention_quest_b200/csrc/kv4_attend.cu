@@ -28,6 +28,13 @@
 // Each warp streams whole records (bulk copies, two blocks per stage) through
 // its own ring in shared memory; the copies of a CTA's next piece are under
 // way while the warps' results of the last one are merged.
+//
+// Measured (B200, 32/8 heads, d = 128, bf16): a 128K context 37.5 us (151 MB, 0.61
+// of the copy rate), of which about 28 streaming and 9 before the first
+// product and in the merges; 1639 of 16384 blocks of a 256K context 14.8 us;
+// 16 rows of 1K to 32K tokens 70 us (0.66). While it streams it is bound by
+// instruction latency: 277 instructions per block and warp, three warps per
+// scheduler at 168 registers (sixteen warps at 128 spill and are slower).
 #include "kv4.cuh"
 
 #include "attend_core.cuh"

@@ -12,8 +12,9 @@ namespace resa {
 // done by one lane on words taken from shared memory. Tokens past the row's
 // length count as zeros (code 0, scale 0, zero 0).
 //
-// Bound by HBM (4 B read and 1.1 B written per element pair) if an element
-// costs less than about 14 instructions; see kv4_codes8 for what that takes.
+// Bound by instruction issue: 128K tokens of 8 heads, d = 128, take 149 us (688
+// MB, 105 us at the copy rate) at 3.0 of 4 instructions per cycle, about 14
+// per 32 elements; see kv4_codes8 for what that takes (with divisions 327 us).
 template <typename T> struct Kv4Raw;
 template <> struct Kv4Raw<__nv_bfloat16> {
   uint4 x;
@@ -161,7 +162,8 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, bool wide, const float
 
 // Records to rows, rounded once to the cache type. One warp per (record, K or
 // V); lane (g, c, m) has the sixteen channels 64g + 16m .. + 15 of four
-// tokens, for values the four of an inverse transpose of nibbles.
+// tokens, for values the four of an inverse transpose of nibbles. Bound by HBM
+// (128K tokens of 8 heads, d = 128: 102 us for 688 MB).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_dequantize_kernel(const uint8_t* __restrict__ kv4,
                                                              T* __restrict__ k, T* __restrict__ v,

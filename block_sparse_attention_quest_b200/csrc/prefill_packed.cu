@@ -30,6 +30,11 @@
 //             block descriptors (one CTA per KV head).
 // While one tile's softmax runs, the other tile's products do.
 //
+// Measured (B200, 32/8 heads, d = 128): 32768 tokens in sequences of 1822,
+// 16384 and 14562 tokens 3630 us = 1092 TFLOP/s, tensor pipe active 62 % of
+// the cycles, the SMs at about 1.34 GHz under the power cap (cuBLAS holds 1390
+// TFLOP/s there); 24 sequences of 0 to 1250 tokens 37 us.
+//
 // Rows of a key tile past the sequence's end belong to other sequences: their
 // scores are masked and their V rows zeroed in shared memory, so nothing of
 // another sequence (an infinity times 0) reaches an output.
@@ -258,123 +263,125 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
   auto tO = [&](int w) { return tmem + 128u * NT + 128u * w; };
 
   if (warp >= 4 * NT) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
-  if (warp == 4 * NT + 1) {
-    // ---------------------------------------------------------------- copies
-    if (lane == 0) {
-      prefetch_tmap(&tmQ);
-      prefetch_tmap(&tmK);
-      prefetch_tmap(&tmV);
-      auto load_q = [&](int w) {
-        mbar_arrive_expect_tx(&bar_q[w], C::kTileBytes);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
+    if (warp == 4 * NT + 1) {
+      // ---------------------------------------------------------------- copies
+      if (lane == 0) {
+        prefetch_tmap(&tmQ);
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+        auto load_q = [&](int w) {
+          mbar_arrive_expect_tx(&bar_q[w], C::kTileBytes);
 #pragma unroll
-        for (int hf = 0; hf < C::kHalves; ++hf)
-          tma_load_3d(sQ(w) + hf * C::kHalfBytes, &tmQ, hf * 64, hg << a.gs, sb.begin + q0 + w * QT,
-                      &bar_q[w]);
-      };
-      load_q(0);
-      int n = 0;                                   // copy n: K (even) or V (odd) of tile n / 2
-      bool ok = true;
-      for (; n < 2 * n_tiles; ++n) {
-        const int i = n % C::kSlots;
-        if (n >= C::kSlots && (n == C::kSlots || (n - C::kSlots) % 2 == 1)) {
-          // the slot's last tile, copy n - 5, is given back with the one
-          // before or after it: K 0 alone first, then V t and K t + 1 together
-          const int f = (n - C::kSlots + 1) / 2;
-          if (!(ok = mbar_wait_bounded(&bar_free[f % 3], (f / 3) & 1, a.ctrl))) break;
-        }
-        mbar_arrive_expect_tx(&bar_full[i], C::kTileBytes);
-        const CUtensorMap* map = n & 1 ? &tmV : &tmK;
-#pragma unroll
-        for (int hf = 0; hf < C::kHalves; ++hf)
-          tma_load_3d(slot(n) + hf * C::kHalfBytes, map, hf * 64, g, sb.begin + (n >> 1) * 128,
-                      &bar_full[i]);
-        if (NT > 1 && n == 0 && nt_b > 0) load_q(NT - 1);
-      }
-      if (!ok) {
-        // the copies in flight end (within the bound) before this CTA does
-        for (int m = n >= C::kSlots ? n - C::kSlots : 0; m < n; ++m)
-          (void)mbar_wait_bounded(&bar_full[m % C::kSlots], (m / C::kSlots) & 1, a.ctrl);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 4 * NT) {
-    // -------------------------------------------------------------- products
-    if (lane == 0) {
-      constexpr uint32_t idS = tc::idesc_bf16(128, 128, false);
-      constexpr uint32_t idO = tc::idesc_bf16(128, D, true);
-      constexpr uint32_t hi = tc::desc_hi(1024);
-      constexpr uint32_t kTileLo = C::kTileBytes >> 4, kHalfLo = C::kHalfBytes >> 4;
-      const uint32_t q_lo = tc::desc_lo(smem_u32(sQ(0)), 16);
-      const uint32_t k_lo = tc::desc_lo(smem_u32(slot(0)), 16);
-      const uint32_t v_lo = tc::desc_lo(smem_u32(slot(0)), C::kHalfBytes);
-      // the ring slot in use and its phase; slots are taken in the order they
-      // are filled: K 0, V 0, K 1, V 1, ...
-      auto qk = [&](int w, uint32_t i) {
-        const uint32_t ql = q_lo + w * kTileLo, kl = k_lo + i * kTileLo, d = tS(w);
-        tc::mma_ss_lo<false>(d, ql, kl, hi, idS);
-#pragma unroll
-        for (int kk = 1; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalfLo + (kk & 3) * 2;
-          tc::mma_ss_lo<true>(d, ql + off, kl + off, hi, idS);
-        }
-        tc::commit(&bar_s[w]);
-      };
-      auto pv = [&](int w, int half, uint32_t i, uint32_t acc) {   // 64 keys
-        const uint32_t vl = v_lo + i * kTileLo + half * 512, d = tO(w), p = tS(w) + 32u * half;
-        tc::mma_ts_lo(d, p, vl, hi, idO, acc);
-#pragma unroll
-        for (int kk = 1; kk < 4; ++kk) tc::mma_ts_lo(d, p + 8u * kk, vl + kk * 128, hi, idO, 1u);
-      };
-      bool ok = mbar_wait_bounded(&bar_full[0], 0, a.ctrl);
-      for (int w = 0; ok && w < (nt_b > 0 ? 2 : 1); ++w) {
-        if (!(ok = mbar_wait_bounded(&bar_q[w], 0, a.ctrl))) break;
-        tc::fence_after_sync();
-        qk(w, 0);
-      }
-      if (ok) tc::commit(&bar_free[0]);
-      uint32_t f = 1;                              // give-back t + 1 on barrier f
-      uint32_t i = 1, ph = 0;                      // slot and phase of V of tile t
-      for (int t = 0; ok && t < n_tiles; ++t) {
-        uint32_t i2 = i + 1, ph2 = ph;             // of K of tile t + 1
-        if (i2 == C::kSlots) { i2 = 0; ph2 ^= 1u; }
-        if (!(ok = mbar_wait_bounded(&bar_full[i], ph, a.ctrl))) break;
-        bool have_k = false;
-#pragma unroll
-        for (int w = 0; w < NT; ++w) {
-          const int nt = w == 0 ? nt_a : nt_b;
-          if (!ok || t >= nt) continue;
-          if (!(ok = mbar_wait_bounded(&bar_p[w][0], t & 1, a.ctrl))) continue;
-          tc::fence_after_sync();
-          pv(w, 0, i, t > 0);
-          if (!(ok = mbar_wait_bounded(&bar_p[w][1], t & 1, a.ctrl))) continue;
-          tc::fence_after_sync();
-          pv(w, 1, i, 1u);
-          if (t + 1 < nt) {
-            if (!have_k) {
-              if (!(ok = mbar_wait_bounded(&bar_full[i2], ph2, a.ctrl))) continue;
-              have_k = true;
-              tc::fence_after_sync();
-            }
-            qk(w, i2);
-          } else {
-            tc::commit(&bar_o[w]);
+          for (int hf = 0; hf < C::kHalves; ++hf)
+            tma_load_3d(sQ(w) + hf * C::kHalfBytes, &tmQ, hf * 64, hg << a.gs, sb.begin + q0 + w * QT,
+                        &bar_q[w]);
+        };
+        load_q(0);
+        int n = 0;                                   // copy n: K (even) or V (odd) of tile n / 2
+        bool ok = true;
+        for (; n < 2 * n_tiles; ++n) {
+          const int i = n % C::kSlots;
+          if (n >= C::kSlots && (n == C::kSlots || (n - C::kSlots) % 2 == 1)) {
+            // the slot's last tile, copy n - kSlots, is given back with the one
+            // before or after it: K 0 alone first, then V t and K t + 1 together
+            const int f = (n - C::kSlots + 1) / 2;
+            if (!(ok = mbar_wait_bounded(&bar_free[f % 3], (f / 3) & 1, a.ctrl))) break;
           }
+          mbar_arrive_expect_tx(&bar_full[i], C::kTileBytes);
+          const CUtensorMap* map = n & 1 ? &tmV : &tmK;
+#pragma unroll
+          for (int hf = 0; hf < C::kHalves; ++hf)
+            tma_load_3d(slot(n) + hf * C::kHalfBytes, map, hf * 64, g, sb.begin + (n >> 1) * 128,
+                        &bar_full[i]);
+          if (NT > 1 && n == 0 && nt_b > 0) load_q(NT - 1);
         }
-        if (!ok) break;
-        // both tiles have taken V of tile t and K of tile t + 1
-        tc::commit(&bar_free[f]);
-        if (++f == 3) f = 0;
-        i = i2 + 1;
-        ph = ph2;
-        if (i == C::kSlots) { i = 0; ph ^= 1u; }
+        if (!ok) {
+          // the copies in flight end (within the bound) before this CTA does
+          for (int w = 0; w < (nt_b > 0 ? 2 : 1); ++w)
+            (void)mbar_wait_bounded(&bar_q[w], 0, a.ctrl);
+          for (int m = n >= C::kSlots ? n - C::kSlots : 0; m < n; ++m)
+            (void)mbar_wait_bounded(&bar_full[m % C::kSlots], (m / C::kSlots) & 1, a.ctrl);
+        }
       }
+      __syncwarp();
+    } else if (warp == 4 * NT) {
+      // -------------------------------------------------------------- products
+      if (lane == 0) {
+        constexpr uint32_t idS = tc::idesc_bf16(128, 128, false);
+        constexpr uint32_t idO = tc::idesc_bf16(128, D, true);
+        constexpr uint32_t hi = tc::desc_hi(1024);
+        constexpr uint32_t kTileLo = C::kTileBytes >> 4, kHalfLo = C::kHalfBytes >> 4;
+        const uint32_t q_lo = tc::desc_lo(smem_u32(sQ(0)), 16);
+        const uint32_t k_lo = tc::desc_lo(smem_u32(slot(0)), 16);
+        const uint32_t v_lo = tc::desc_lo(smem_u32(slot(0)), C::kHalfBytes);
+        // the ring slot in use and its phase; slots are taken in the order they
+        // are filled: K 0, V 0, K 1, V 1, ...
+        auto qk = [&](int w, uint32_t i) {
+          const uint32_t ql = q_lo + w * kTileLo, kl = k_lo + i * kTileLo, d = tS(w);
+          tc::mma_ss_lo<false>(d, ql, kl, hi, idS);
+#pragma unroll
+          for (int kk = 1; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalfLo + (kk & 3) * 2;
+            tc::mma_ss_lo<true>(d, ql + off, kl + off, hi, idS);
+          }
+          tc::commit(&bar_s[w]);
+        };
+        auto pv = [&](int w, int half, uint32_t i, uint32_t acc) {   // 64 keys
+          const uint32_t vl = v_lo + i * kTileLo + half * 512, d = tO(w), p = tS(w) + 32u * half;
+          tc::mma_ts_lo(d, p, vl, hi, idO, acc);
+#pragma unroll
+          for (int kk = 1; kk < 4; ++kk) tc::mma_ts_lo(d, p + 8u * kk, vl + kk * 128, hi, idO, 1u);
+        };
+        bool ok = mbar_wait_bounded(&bar_full[0], 0, a.ctrl);
+        for (int w = 0; ok && w < (nt_b > 0 ? 2 : 1); ++w) {
+          if (!(ok = mbar_wait_bounded(&bar_q[w], 0, a.ctrl))) break;
+          tc::fence_after_sync();
+          qk(w, 0);
+        }
+        if (ok) tc::commit(&bar_free[0]);
+        uint32_t f = 1;                              // give-back t + 1 on barrier f
+        uint32_t i = 1, ph = 0;                      // slot and phase of V of tile t
+        for (int t = 0; ok && t < n_tiles; ++t) {
+          uint32_t i2 = i + 1, ph2 = ph;             // of K of tile t + 1
+          if (i2 == C::kSlots) { i2 = 0; ph2 ^= 1u; }
+          if (!(ok = mbar_wait_bounded(&bar_full[i], ph, a.ctrl))) break;
+          bool have_k = false;
+#pragma unroll
+          for (int w = 0; w < NT; ++w) {
+            const int nt = w == 0 ? nt_a : nt_b;
+            if (!ok || t >= nt) continue;
+            if (!(ok = mbar_wait_bounded(&bar_p[w][0], t & 1, a.ctrl))) continue;
+            tc::fence_after_sync();
+            pv(w, 0, i, t > 0);
+            if (!(ok = mbar_wait_bounded(&bar_p[w][1], t & 1, a.ctrl))) continue;
+            tc::fence_after_sync();
+            pv(w, 1, i, 1u);
+            if (t + 1 < nt) {
+              if (!have_k) {
+                if (!(ok = mbar_wait_bounded(&bar_full[i2], ph2, a.ctrl))) continue;
+                have_k = true;
+                tc::fence_after_sync();
+              }
+              qk(w, i2);
+            } else {
+              tc::commit(&bar_o[w]);
+            }
+          }
+          if (!ok) break;
+          // both tiles have taken V of tile t and K of tile t + 1
+          tc::commit(&bar_free[f]);
+          if (++f == 3) f = 0;
+          i = i2 + 1;
+          ph = ph2;
+          if (i == C::kSlots) { i = 0; ph ^= 1u; }
+        }
+      }
+      __syncwarp();
+    } else if ((hg << a.gs) % a.G == 0) {
+      // ------------------------------------------------- caches and descriptors
+      fill_cache<D>(a, warp == 4 * NT + 3, b, sb.begin, g, q0, nq);
     }
-    __syncwarp();
-  } else if ((hg << a.gs) % a.G == 0) {
-    // ------------------------------------------------- caches and descriptors
-    fill_cache<D>(a, warp == 4 * NT + 3, b, sb.begin, g, q0, nq);
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
     // --------------------------------------------------------------- softmax
