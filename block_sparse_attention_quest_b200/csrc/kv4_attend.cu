@@ -78,9 +78,10 @@ template <typename T, int D>
 struct Kv4Cfg {
   static constexpr int kRec = kv4_record_bytes(D);
   static constexpr int kRing = kKv4Warps<T> * kKv4Stages * 2 * kRec;
-  static constexpr int kMerge = merge_floats(D, kKv4Warps<T>) * 4;
-  static constexpr int kSmem = kRing + kMerge;
-  static_assert(kMerge >= (8 * (kKv4MaxCtas + 2) + 8) * 4, "weights of the parts");
+  // the warps' results; then the parts' weights and the threads' sums
+  static constexpr int kWarps = merge_floats(D, kKv4Warps<T>) * 4;
+  static constexpr int kParts = (8 * (kKv4MaxCtas + 2) + 8 + kKv4Warps<T> * 32 * 4) * 4;
+  static constexpr int kSmem = kRing + (kWarps > kParts ? kWarps : kParts);
 };
 
 // blocks of row b that its heads attend to
@@ -140,10 +141,20 @@ __device__ __forceinline__ void kv4_find(const Kv4K& a, uint32_t x, uint32_t& to
   total = run;
 }
 
+// 2^x; results below 2^-126 are 0 (weights that small change no sum here)
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Merge of the partials that `parts` consecutive CTAs from `first` on left of one
 // (row, head), by one CTA. `late`: the first of them began before this (row,
 // head), so it is that CTA's last piece. The (max, sum) pairs are turned into
 // weights first, then every thread sums pairs of output columns over the parts.
+// (Code that a CTA runs once costs its fetch, some 25 cycles an instruction,
+// far more than its execution: loops here and in the rest of a piece's end are
+// kept rolled.)
 template <typename T, int D>
 __device__ __forceinline__ void kv4_merge(const Kv4K& a, float* sm, int first, int parts,
                                           bool late, int64_t head0) {
@@ -152,55 +163,62 @@ __device__ __forceinline__ void kv4_merge(const Kv4K& a, float* sm, int first, i
   auto slot = [&](int s) -> int { return 2 * (first + s) + (s == 0 && late ? 1 : 0); };
   float* w_s = sm;                      // [parts][8] weights
   float* l_h = sm + 8 * (kKv4MaxCtas + 2);
-  for (int h = warp; h < a.G; h += NW) {
-    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + h;
-    // (the usual number of parts is at most 32: one load per lane)
-    const float2 mine = lane < parts ? __ldcg(ml + slot(lane) * a.G) : make_float2(-INFINITY, 0.f);
-    float m = mine.x;
-    for (int s = lane + 32; s < parts; s += 32) m = fmaxf(m, __ldcg(ml + slot(s) * a.G).x);
-    m = warp_max_xor(m, 16, 1);
+  float4* sums = reinterpret_cast<float4*>(l_h + 8);
+  if (warp < a.G) {
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + warp;
+    float m = -INFINITY;
+#pragma unroll 1
+    for (int s = lane; s < parts; s += 32) m = fmaxf(m, __ldcg(ml + slot(s) * a.G).x);
+#pragma unroll 1
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.f;
+#pragma unroll 1
     for (int s = lane; s < parts; s += 32) {
-      const float2 p = s == lane ? mine : __ldcg(ml + slot(s) * a.G);
-      const float w = p.x == -INFINITY ? 0.f : exp2f(p.x - m);
-      w_s[s * 8 + h] = w;
+      const float2 p = __ldcg(ml + slot(s) * a.G);
+      const float w = p.x == -INFINITY ? 0.f : ex2_ftz(p.x - m);
+      w_s[s * 8 + warp] = w;
       l = fmaf(w, p.y, l);
     }
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
-      l_h[h] = l;
-      if (a.lse != nullptr) a.lse[head0 + h] = (m + log2f(l)) * 0.69314718055994531f;
+      l_h[warp] = l;
+      if (a.lse != nullptr) a.lse[head0 + warp] = (m + log2f(l)) * 0.69314718055994531f;
     }
   }
-  T* out = static_cast<T*>(a.out);
-  for (int i0 = 0; i0 < a.G * (D / 2); i0 += NT) {
-    const int i = i0 + threadIdx.x;
-    const bool in = i < a.G * (D / 2);
-    const int h = i / (D / 2), c = (i % (D / 2)) * 2;
-    const float* po = a.part_o + h * D + c;
-    float o0 = 0.f, o1 = 0.f;
-    for (int s0 = 0; s0 < parts; s0 += 24) {
-      float2 x[24];
-#pragma unroll
-      for (int u = 0; u < 24; ++u)
-        if (in && s0 + u < parts)
-          x[u] = __ldcg(reinterpret_cast<const float2*>(
-              po + static_cast<int64_t>(slot(s0 + u)) * a.G * D));
-      if (i0 == 0 && s0 == 0) __syncthreads();     // the weights, behind the first loads
-#pragma unroll
-      for (int u = 0; u < 24; ++u)
-        if (in && s0 + u < parts) {
-          const float w = w_s[(s0 + u) * 8 + h];
-          o0 = fmaf(w, x[u].x, o0);
-          o1 = fmaf(w, x[u].y, o1);
-        }
+  __syncthreads();
+  // four columns per thread; where the group's columns need fewer threads than
+  // there are, every `step`-th part
+  const int items = a.G * (D / 4), step = NT / items > 0 ? NT / items : 1;
+  for (int i0 = 0; i0 < items; i0 += NT) {
+    const int i = i0 + static_cast<int>(threadIdx.x) % (items < NT ? items : NT);
+    const int from = threadIdx.x / (items < NT ? items : NT);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < items && from < step) {
+      const int h = i / (D / 4);
+      const float4* po = reinterpret_cast<const float4*>(a.part_o) + i;
+#pragma unroll 4
+      for (int s = from; s < parts; s += step) {
+        const float4 x = __ldcg(po + static_cast<int64_t>(slot(s)) * items);
+        const float w = w_s[s * 8 + h];
+        y.x = fmaf(w, x.x, y.x); y.y = fmaf(w, x.y, y.y);
+        y.z = fmaf(w, x.z, y.z); y.w = fmaf(w, x.w, y.w);
+      }
     }
-    if (in) {
-      const float inv = 1.f / l_h[h];
-      out[(head0 + h) * D + c] = Dt<T>::from_f(o0 * inv);
-      out[(head0 + h) * D + c + 1] = Dt<T>::from_f(o1 * inv);
+    sums[threadIdx.x] = y;
+    __syncthreads();
+    if (i < items && from == 0) {
+#pragma unroll 1
+      for (int k = 1; k < step; ++k) {
+        const float4 x = sums[threadIdx.x + k * items];
+        y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+      }
+      const float inv = 1.f / l_h[i / (D / 4)];
+      T* out = static_cast<T*>(a.out) + head0 * D + i * 4;
+      out[0] = Dt<T>::from_f(y.x * inv); out[1] = Dt<T>::from_f(y.y * inv);
+      out[2] = Dt<T>::from_f(y.z * inv); out[3] = Dt<T>::from_f(y.w * inv);
     }
+    __syncthreads();
   }
 }
 
@@ -238,13 +256,6 @@ __device__ __forceinline__ void mma_row0(float& d0, float& d1, const uint32_t (&
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// 2^x; results below 2^-126 are 0 (weights that small change no sum here)
-__device__ __forceinline__ float ex2_ftz(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // A warp takes two blocks at a time (one stage of its ring): the two
 // independent chains of products and exponentials hide each other's latency,
 // and the barrier, the check of the running maximum and the loop's own
@@ -275,6 +286,7 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
   constexpr float kUp = PARTS == 1 ? 18446744073709551616.f : 1.f;
   constexpr float kDown = 5.9029581035870565e+20f;              // 2^69
   constexpr uint32_t kOnes = 0x00010001u;                       // code 1 in both halves
+  constexpr uint32_t kOne = PARTS == 1 ? kOnes : 0x3f803f80u, kOneHigh = PARTS == 1 ? 0x00100010u : kOne;
   constexpr float kMid = 8.f;                                   // code the products are taken about
   constexpr float kMidK = PARTS == 1 ? 0.f : 8.f;
   constexpr float kKeys = PARTS == 1 ? kDown : 1.f;             // what brings q . code back
@@ -450,7 +462,6 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
       // times too large), step 2j + 1 nibbles 2, 6 and 3, 7
 #pragma unroll
       for (int g2 = 0; g2 < NG; ++g2) {
-        float sum = 0.f;
         if constexpr (PARTS == 1) {
           uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
           if (gq < a.G) {
@@ -459,10 +470,6 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float f[8];
-            Chunk<__nv_bfloat16>::unpack(raw[j], f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum += f[i];
             const uint32_t lo[2] = {raw[j].x, raw[j].y}, hi[2] = {raw[j].z, raw[j].w};
 #pragma unroll
             for (int s = 0; s < 2; ++s) {          // times 2^64 and 2^60, exact
@@ -477,8 +484,6 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = 0.f;
             if (gq < a.G) load8<T>(qg + g2 * 64 + j * 8, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum += f[i];
             float part[8][PARTS];
 #pragma unroll
             for (int i = 0; i < 8; ++i) bf16_parts<PARTS>(f[i], part[i]);
@@ -491,11 +496,17 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
               }
           }
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        // heads 2 cq and 2 cq + 1 of the result layout, in the sums' scale
-        qs0[g2] = __shfl_sync(0xffffffffu, sum, 8 * cq) * (1.f / kKeys);
-        qs1[g2] = __shfl_sync(0xffffffffu, sum, 8 * cq + 4) * (1.f / kKeys);
+        // the sums of q of heads 2 cq and 2 cq + 1, as the products with codes
+        // of 1 (read as 16 where codes are), in the logits' scale
+        const uint32_t one[4] = {kOne, kOne, kOneHigh, kOneHigh};
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = PARTS - 1; p >= 0; --p)
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            mma_bf16_16816(acc, one, qb[p][g2 * 4 + s][0], qb[p][g2 * 4 + s][1]);
+        qs0[g2] = acc[0];
+        qs1[g2] = acc[1];
       }
     }
     const float to_log2 = a.scale_log2 * kKeys;
@@ -701,19 +712,18 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     }
     if (!more) grid_launch_dependents();
     // ---- the warps' results, merged in shared memory
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 4);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 8);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 16);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 4);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 8);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 16);
+#pragma unroll 1
+    for (int m = 4; m <= 16; m <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, m);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, m);
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-#pragma unroll
-      for (int m = 4; m <= 16; m <<= 1) {
+      for (int i = 0; i < NG; ++i) {
         zo0[i] += __shfl_xor_sync(0xffffffffu, zo0[i], m);
         zo1[i] += __shfl_xor_sync(0xffffffffu, zo1[i], m);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
       zo0[i] *= 1.f / kUp;
       zo1[i] *= 1.f / kUp;
     }
@@ -748,11 +758,13 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     }
     if (warp < 8) {                               // head `warp`: lane w holds warp w's (m, l)
       const float m = lane < NW ? sm_m[lane * 8 + warp] : -INFINITY;
-      const float mx = warp_max_xor(m, 16, 1);
+      float mx = m;
+#pragma unroll 1
+      for (int i = 8; i >= 1; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
       const float w = m == -INFINITY ? 0.f : ex2_ftz(m - mx);
       float l = lane < NW ? w * sm_l[lane * 8 + warp] : 0.f;
-#pragma unroll
-      for (int i = 16; i >= 1; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+#pragma unroll 1
+      for (int i = 8; i >= 1; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
       __syncwarp();
       if (lane < NW) sm_m[lane * 8 + warp] = w;
       if (lane == 0) { s_mx[warp] = mx; s_l[warp] = l; }
