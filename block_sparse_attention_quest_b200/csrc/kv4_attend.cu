@@ -29,10 +29,10 @@
 // its own ring in shared memory; the copies of a CTA's next piece are under
 // way while the warps' results of the last one are merged.
 //
-// Measured (B200, 32/8 heads, d = 128, bf16): a 128K context 37.5 us (151 MB, 0.61
-// of the copy rate), of which about 28 streaming and 9 before the first
-// product and in the merges; 1639 of 16384 blocks of a 256K context 14.8 us;
-// 16 rows of 1K to 32K tokens 70 us (0.66). While it streams it is bound by
+// Measured (B200, 32/8 heads, d = 128, bf16): a 128K context 35.3 us (151 MB, 0.65
+// of the copy rate), of which about 27 streaming and 8 before the first
+// product and in the merges; 1639 of 16384 blocks of a 256K context 14.4 us;
+// 16 rows of 1K to 32K tokens 67.6 us (0.69). While it streams it is bound by
 // instruction latency: 277 instructions per block and warp, three warps per
 // scheduler at 168 registers (sixteen warps at 128 spill and are slower).
 #include "kv4.cuh"
@@ -69,9 +69,9 @@ constexpr int kKv4Warps = sizeof(T) == 2 ? 12 : 8;
 constexpr int kKv4Stages = 3;      // stages of two records per warp
 constexpr int kKv4MinBlocks = 16;  // blocks per CTA below which fewer CTAs are used
 // A piece's fixed cost, in blocks: its q, its first records' latency and the
-// merge of its warps, measured at 4.6 us where a block takes 72 ns (a batch of
-// 16 rows of 1K to 32K tokens; with 24 the CTAs of several short rows ended
-// last, 37 us after those of one long row).
+// merge of its warps, 4 us or more where a block takes 72 ns. Measured back to
+// back on a batch of 16 rows of 1K to 32K tokens: 69.4 us with 32, 64.4 with 48,
+// 64.1 with 64 (with less the CTAs of several short rows end last).
 constexpr uint32_t kKv4PieceCost = 64;
 
 template <typename T, int D>
