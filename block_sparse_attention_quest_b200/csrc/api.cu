@@ -828,6 +828,7 @@ static int check_kv4_decode(const resa_dims* dims, Shape* s, const void* q, cons
       len < 1 || !(softmax_scale > 0.f && softmax_scale < 1e17f))   // (its product with 2^69 is finite)
     return RESA_ERR_INVALID_ARG;
   if (len > s->L_max) return RESA_ERR_CAPACITY;
+  if (!kv4_range_fits(*s, blocks_of(len))) return RESA_ERR_UNSUPPORTED;
   if (workspace_bytes < kv4_layout(*s, len).total) return RESA_ERR_WORKSPACE;
   return RESA_OK;
 }

@@ -92,8 +92,7 @@ __device__ __forceinline__ uint32_t kv4_row_blocks(const Kv4K& a, int b) {
 }
 
 // The range of all (row, head) units, each kKv4PieceCost + its blocks long, and
-// its cut into equal parts (positions stay below 2^32: a cache has fewer than
-// 2^31 rows).
+// its cut into equal parts (positions stay below 2^32: kv4_range_fits).
 struct Kv4Range {
   uint32_t total, per, rem;
   int ctas;
@@ -869,6 +868,12 @@ int kv4_most_ctas(const Shape& s, int64_t blocks_bound) {
   const int64_t want = (blocks_bound + kKv4MinBlocks - 1) / kKv4MinBlocks;
   const int64_t n = static_cast<int64_t>(s.B) * s.H * (want < kMaxSplits ? want : kMaxSplits);
   return static_cast<int>(n < kKv4MaxCtas ? n : kKv4MaxCtas);
+}
+
+// (a cache of fewer than 2^31 rows can still have some 2^26 units of a block or
+// two, whose fixed costs add up to more)
+bool kv4_range_fits(const Shape& s, int64_t blocks_bound) {
+  return static_cast<int64_t>(s.B) * s.H * (blocks_bound + kKv4PieceCost) < (1LL << 32);
 }
 
 cudaError_t launch_kv4_attend(const Shape& s, const Kv4Args& a, cudaStream_t st) {

@@ -213,6 +213,8 @@ constexpr int kKv4MaxCtas = 512;
 // with per-row lengths
 int kv4_ctas(const Shape& s, int64_t blocks_bound, bool ragged, int num_sms, int* splits);
 int kv4_most_ctas(const Shape& s, int64_t blocks_bound);
+// whether the positions of such a launch's range fit 32 bits
+bool kv4_range_fits(const Shape& s, int64_t blocks_bound);
 
 // bounded wait of one thread until *flag >= target (failure-detection check)
 cudaError_t launch_wait_check(const int* flag, int target, unsigned long long limit_ns,

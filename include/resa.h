@@ -420,7 +420,8 @@ RESA_API int resa_kv4_dequantize(const resa_dims* dims, const void* kv4, int64_t
 /* resa_decode_dense on a 4-bit cache: if k_new != NULL, k_new/v_new are
  * quantised into slot len-1 (and k_new merged into its block's descriptor when
  * desc != NULL); then attention over the values the records of every token
- * < len stand for. */
+ * < len stand for. This call and the two below return RESA_ERR_UNSUPPORTED
+ * where batch * n_kv_heads * (blocks of len + 64) reaches 2^32. */
 RESA_API int resa_decode_dense_kv4(const resa_dims* dims, const void* q, const void* k_new,
                                    const void* v_new, void* kv4, void* desc, int64_t len,
                                    const int32_t* lens, float softmax_scale, void* out, float* lse,

@@ -106,6 +106,13 @@ def test_sparse_kv4_refuses_more_blocks_than_a_selection_takes(resa):
     assert kv4_call(resa, "sparse", d=d, n=16 * 262144 + 1) == resa.RESA_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("f", ["dense", "sparse", "blocks"])
+def test_kv4_refuses_more_heads_than_its_work_split_can_number(resa, f):
+    # 65535 x 1024 heads of one block: 65 positions each, more than 2^32 in all
+    d = dims(resa, batch=65535, n_q_heads=1024, n_kv_heads=1024, max_len=16)
+    assert kv4_call(resa, f, d=d, n=16, n_sel=1, wsb=1 << 60) == resa.RESA_ERR_UNSUPPORTED
+
+
 def test_weights_refusals(resa):
     lib, E = resa._lib, resa
 
