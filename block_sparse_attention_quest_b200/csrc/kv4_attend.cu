@@ -29,10 +29,10 @@
 // its own ring in shared memory; the copies of a CTA's next piece are under
 // way while the warps' results of the last one are merged.
 //
-// Measured (B200, 32/8 heads, d = 128, bf16): a 128K context 35.3 us (151 MB, 0.65
+// Measured (B200, 32/8 heads, d = 128, bf16): a 128K context 35.0 us (151 MB, 0.66
 // of the copy rate), of which about 27 streaming and 8 before the first
-// product and in the merges; 1639 of 16384 blocks of a 256K context 14.4 us;
-// 16 rows of 1K to 32K tokens 67.6 us (0.69). While it streams it is bound by
+// product and in the merges; 1639 of 16384 blocks of a 256K context 14.1 us;
+// 16 rows of 1K to 32K tokens 66.4 us (0.70). While it streams it is bound by
 // instruction latency: 277 instructions per block and warp, three warps per
 // scheduler at 168 registers (sixteen warps at 128 spill and are slower).
 #include "kv4.cuh"
@@ -150,7 +150,7 @@ __device__ __forceinline__ float ex2_ftz(float x) {
 // Merge of the partials that `parts` consecutive CTAs from `first` on left of one
 // (row, head), by one CTA. `late`: the first of them began before this (row,
 // head), so it is that CTA's last piece. The (max, sum) pairs are turned into
-// weights first, then every thread sums pairs of output columns over the parts.
+// weights first, then every thread sums four output columns over its parts.
 // (Code that a CTA runs once costs its fetch, some 25 cycles an instruction,
 // far more than its execution: loops here and in the rest of a piece's end are
 // kept rolled.)
@@ -163,17 +163,35 @@ __device__ __forceinline__ void kv4_merge(const Kv4K& a, float* sm, int first, i
   float* w_s = sm;                      // [parts][8] weights
   float* l_h = sm + 8 * (kKv4MaxCtas + 2);
   float4* sums = reinterpret_cast<float4*>(l_h + 8);
+  // four columns per thread; where the group's columns need fewer threads than
+  // there are, every `step`-th part. The first four of a thread's parts are
+  // requested ahead of the weights (eight make the kernel spill: 35.9 us at 128K
+  // against 35.0; none 35.3).
+  static_assert(8 * (D / 4) <= NT, "a thread has at most four columns");
+  constexpr int kAhead = 4;
+  const int items = a.G * (D / 4), step = NT / items;
+  const int i = static_cast<int>(threadIdx.x) % items, from = static_cast<int>(threadIdx.x) / items;
+  const int most = from < step ? parts : 0;
+  const float4* po = reinterpret_cast<const float4*>(a.part_o) + i;
+  float4 x[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int s = from + u * step;
+    if (s < most) x[u] = __ldcg(po + static_cast<int64_t>(slot(s)) * items);
+  }
   if (warp < a.G) {
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + warp;
-    float m = -INFINITY;
+    // (mostly at most 32 parts: one load per lane)
+    const float2 mine = lane < parts ? __ldcg(ml + slot(lane) * a.G) : make_float2(-INFINITY, 0.f);
+    float m = mine.x;
 #pragma unroll 1
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, __ldcg(ml + slot(s) * a.G).x);
+    for (int s = lane + 32; s < parts; s += 32) m = fmaxf(m, __ldcg(ml + slot(s) * a.G).x);
 #pragma unroll 1
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.f;
 #pragma unroll 1
     for (int s = lane; s < parts; s += 32) {
-      const float2 p = __ldcg(ml + slot(s) * a.G);
+      const float2 p = s == lane ? mine : __ldcg(ml + slot(s) * a.G);
       const float w = p.x == -INFINITY ? 0.f : ex2_ftz(p.x - m);
       w_s[s * 8 + warp] = w;
       l = fmaf(w, p.y, l);
@@ -186,39 +204,34 @@ __device__ __forceinline__ void kv4_merge(const Kv4K& a, float* sm, int first, i
     }
   }
   __syncthreads();
-  // four columns per thread; where the group's columns need fewer threads than
-  // there are, every `step`-th part
-  const int items = a.G * (D / 4), step = NT / items > 0 ? NT / items : 1;
-  for (int i0 = 0; i0 < items; i0 += NT) {
-    const int i = i0 + static_cast<int>(threadIdx.x) % (items < NT ? items : NT);
-    const int from = threadIdx.x / (items < NT ? items : NT);
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < items && from < step) {
-      const int h = i / (D / 4);
-      const float4* po = reinterpret_cast<const float4*>(a.part_o) + i;
-#pragma unroll 4
-      for (int s = from; s < parts; s += step) {
-        const float4 x = __ldcg(po + static_cast<int64_t>(slot(s)) * items);
-        const float w = w_s[s * 8 + h];
-        y.x = fmaf(w, x.x, y.x); y.y = fmaf(w, x.y, y.y);
-        y.z = fmaf(w, x.z, y.z); y.w = fmaf(w, x.w, y.w);
-      }
-    }
-    sums[threadIdx.x] = y;
-    __syncthreads();
-    if (i < items && from == 0) {
-#pragma unroll 1
-      for (int k = 1; k < step; ++k) {
-        const float4 x = sums[threadIdx.x + k * items];
-        y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
-      }
-      const float inv = 1.f / l_h[i / (D / 4)];
-      T* out = static_cast<T*>(a.out) + head0 * D + i * 4;
-      out[0] = Dt<T>::from_f(y.x * inv); out[1] = Dt<T>::from_f(y.y * inv);
-      out[2] = Dt<T>::from_f(y.z * inv); out[3] = Dt<T>::from_f(y.w * inv);
-    }
-    __syncthreads();
+  const int h = i / (D / 4);
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& z, float w) {
+    y.x = fmaf(w, z.x, y.x); y.y = fmaf(w, z.y, y.y);
+    y.z = fmaf(w, z.z, y.z); y.w = fmaf(w, z.w, y.w);
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int s = from + u * step;
+    if (s < most) add(x[u], w_s[s * 8 + h]);
   }
+#pragma unroll 1
+  for (int s = from + kAhead * step; s < most; s += step)
+    add(__ldcg(po + static_cast<int64_t>(slot(s)) * items), w_s[s * 8 + h]);
+  sums[threadIdx.x] = y;
+  __syncthreads();
+  if (from == 0) {
+#pragma unroll 1
+    for (int k = 1; k < step; ++k) {
+      const float4 z = sums[threadIdx.x + k * items];
+      y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+    }
+    const float inv = 1.f / l_h[h];
+    T* out = static_cast<T*>(a.out) + head0 * D + i * 4;
+    out[0] = Dt<T>::from_f(y.x * inv); out[1] = Dt<T>::from_f(y.y * inv);
+    out[2] = Dt<T>::from_f(y.z * inv); out[3] = Dt<T>::from_f(y.w * inv);
+  }
+  __syncthreads();
 }
 
 // A value as the sum of PARTS bf16 numbers (the first is its rounding, each
