@@ -394,7 +394,9 @@ __global__ void __launch_bounds__(NW * 32) attend_f32_keep_kernel(AttnK a) {
 #pragma unroll
     for (int h = 0; h < 8; ++h)
       if (h < a.G) {
-        z[h] = exp2f(z[h] - m[h]);                // the weight from here on
+        // the weight from here on (0 in a warp whose logits so far are all
+        // minus infinity, as an overflow leaves them)
+        z[h] = exp2f(z[h] - (m[h] == -INFINITY ? 0.f : m[h]));
         l[h] += z[h];
       }
     // ---- values: lane's channels CPL * lane ..

@@ -326,9 +326,14 @@ __device__ __forceinline__ bool stream_bf16(const CUtensorMap* tmK, const CUtens
     mx0 = warp_max_xor(mx0, 16, 4);
     mx1 = warp_max_xor(mx1, 16, 4);
     const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-    const float al0 = exp2f(m0 - mn0), al1 = exp2f(m1 - mn1);
-    const float p0 = exp2f(s0 - mn0), p2 = exp2f(s2 - mn0);
-    const float p1 = exp2f(s1 - mn1), p3 = exp2f(s3 - mn1);
+    float r0 = mn0, r1 = mn1;
+    if constexpr (kKeep) {                       // logits so far all minus infinity: weights 0
+      r0 = mn0 == -INFINITY ? 0.f : mn0;
+      r1 = mn1 == -INFINITY ? 0.f : mn1;
+    }
+    const float al0 = exp2f(m0 - r0), al1 = exp2f(m1 - r1);
+    const float p0 = exp2f(s0 - r0), p2 = exp2f(s2 - r0);
+    const float p1 = exp2f(s1 - r1), p3 = exp2f(s3 - r1);
     l0 = fmaf(l0, al0, p0 + p2);
     l1 = fmaf(l1, al1, p1 + p3);
     m0 = mn0;

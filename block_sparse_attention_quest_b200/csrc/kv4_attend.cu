@@ -532,7 +532,9 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
       zo0[i] = 0.f; zo1[i] = 0.f;
     }
     // n = kOff - m with m the reference (log2 units) of the weights 2^(s + n)
-    float n0 = INFINITY, n1 = INFINITY, l0 = 0.f, l1 = 0.f;
+    // (finite: logits of minus infinity, as an overflow of fp32 leaves them,
+    // weigh 0 before any other has come)
+    float n0 = 3.4e38f, n1 = 3.4e38f, l0 = 0.f, l1 = 0.f;
 
     int k = 0;
     for (; k < count; ++k) {
@@ -637,12 +639,10 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
         for (int e = 0; e < 4; ++e) s[u][e] = __fmul_rn(s[u][e], to_log2);
       const float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
       const float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
-      // (n = infinity before the first pair, where the sum is infinite or NaN)
       if (__any_sync(0xffffffffu, !(x0 + n0 <= kOff + 8.f && x1 + n1 <= kOff + 8.f))) {
         const float r0 = fminf(n0, kOff - warp_max_xor(x0, 16, 4));
         const float r1 = fminf(n1, kOff - warp_max_xor(x1, 16, 4));
-        const float al0 = n0 == INFINITY ? 0.f : ex2_ftz(r0 - n0);
-        const float al1 = n1 == INFINITY ? 0.f : ex2_ftz(r1 - n1);
+        const float al0 = ex2_ftz(r0 - n0), al1 = ex2_ftz(r1 - n1);
         n0 = r0; n1 = r1;
         l0 *= al0; l1 *= al1;
 #pragma unroll

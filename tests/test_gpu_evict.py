@@ -117,6 +117,35 @@ def test_weights_of_a_step(resa, dtype, d, G, lens, ragged):
     assert dtype == "f32" or torch.equal(out, o2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logits_below_the_fp32_range_weigh_nothing(resa, dtype):
+    # tokens 0 .. 31 (the first blocks of two warps): logits near -1e39; the
+    # others' keys leave channel 0 out
+    B, H, G, d, n, scale = 1, 2, 4, 128, 64, 1.0 / math.sqrt(128)
+    k, v = rnd(1, B, H, n, d, dtype=dtype), rnd(2, B, H, n, d, dtype=dtype)
+    q = rnd(3, B, H * G, d, dtype=dtype)
+    k[..., 0] = 0.0
+    k[:, :, :32, 0], q[:, :, 0] = ops.bf16_round(np.float32(-1e22)), ops.bf16_round(np.float32(1e18))
+    kt, vt, qt = dev(k, dtype), dev(v, dtype), dev(q, dtype)
+    wt = torch.zeros(B, H, n, device="cuda")
+    out, lse = torch.empty_like(qt), torch.empty(B, H * G, device="cuda")
+    ws = resa.alloc_weights_workspace(resa.dims_for(kt, H * G), n)
+    resa.decode_dense_weights(qt, None, None, kt, vt, None, wt, n, scale, out, lse, ws)
+    assert resa.workspace_status(ws) == resa.RESA_OK
+    got, on = wt.double().cpu().numpy(), out.double().cpu().numpy()
+    q[:, :, 0] = 0.0
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24   # a rounding of a weight, of an output
+    for h in range(H):
+        qs = q[0, h * G:(h + 1) * G].astype(np.float64)
+        kf, vf = k[0, h, 32:].astype(np.float64), v[0, h, 32:].astype(np.float64)
+        o, _, w = ops.attend_row(qs, kf, vf, scale)
+        rel = max(weight_bounds(qs[i], kf, w[i], scale) for i in range(G))
+        assert (got[0, h, :32] == 0).all()
+        assert (np.abs(got[0, h, 32:] - w.sum(0)) <= rel * w.sum(0) + 1e-37).all()
+        tol = (rel + 1.01 * half + 96 * 2.0 ** -24) * (w @ np.abs(vf)) + half * np.abs(o)
+        assert (np.abs(on[0, h * G:(h + 1) * G] - o) <= tol).all()
+
+
 # --------------------------------------------------------------------- eviction
 
 def run_evict(resa, k, v, w, lens, budget, recent, dtype, cap_out, bound=None, sentinel=3.0):

@@ -222,6 +222,27 @@ def run_dense(resa, B, H, G, d, dtype, lens, cap, seed=5, bound=None, stale=True
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logits_below_the_fp32_range_weigh_nothing(resa, dtype):
+    # tokens 0 .. 31 (one warp's pair of blocks): logits of -1e39 by a scale of
+    # 1000, which q makes up for elsewhere; the others' keys leave channel 0 out
+    B, H, G, d, n, scale = 1, 2, 4, 128, 64, 1000.0
+    k, v = rnd(1, B, H, n, d, dtype=dtype), rnd(2, B, H, n, d, dtype=dtype)
+    q = ops.bf16_round(rnd(3, B, H * G, d) / np.float32(1000 * math.sqrt(d)))
+    k[:, :, :, :64], q[:, :, :64] = 0.0, 0.0
+    k[:, :, :32, 0], q[:, :, 0] = ops.bf16_round(np.float32(-1e18)), ops.bf16_round(np.float32(1e18))
+    rec = torch.zeros(B, H, n // 16, ops.kv4_record_bytes(d), dtype=torch.uint8, device="cuda")
+    resa.kv4_quantize(dev(k, dtype), dev(v, dtype), n, rec, H * G)
+    qt = dev(q, dtype)
+    out, lse = torch.empty_like(qt), torch.empty(B, H * G, device="cuda")
+    ws = resa.alloc_kv4_workspace(resa.dims_kv4(rec, qt), n)
+    resa.decode_dense_kv4(qt, None, None, rec, None, n, scale, out, ws, lse=lse)
+    assert resa.workspace_status(ws) == resa.RESA_OK
+    q[:, :, 0] = 0.0
+    check(resa, q, rec.cpu().numpy()[:, :, 2:], [32], None, out.double().cpu().numpy(),
+          lse.double().cpu().numpy(), scale, dtype, d, H)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G", [1, 3, 4, 8])
 @pytest.mark.parametrize("n", [1, 15, 16, 17, 129, 1000])
