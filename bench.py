@@ -50,8 +50,8 @@ METRIC = "ReSA decode-step us & achieved HBM GB/s vs roofline at 128K/256K; rect
 #     rectify_tc_kernel at 128K, f = 32 (--set full, one cold launch).
 NCU_COUNTERS = {
     "attention": {"files": ["attend.cu", "attend_core.cuh", "common.cuh", "launch.h"],
-                  "source": "6db97d0b069c9689",
-                  "traffic": {"resa_decode_128k_b1": 53945088}},
+                  "source": "a5d57e97488fbfaf",
+                  "traffic": {"resa_decode_128k_b1": 53942016}},
     "rectify": {"files": ["rectify_tc.cu", "tc.cuh", "common.cuh", "launch.h"], "source": "2bf9fdade30738eb",
                 "tensor_pipe_active_pct": 36.22, "traffic": 541861888},
 }
