@@ -8,9 +8,9 @@
 // 8 heads, then 16 channels x 8 heads), and the scales and zeros enter as fp32
 // factors of the sums, two per token and head. A code is used as the bf16
 // subnormal its bits are (code * 2^-133): one mask per two codes and no
-// conversion; q and p enter multiplied by 2^64 so that every sum stays a
-// normal number, and 2^69 is taken out of the results. Codes, q (bf16) and
-// their products are exact. p * vs is rounded to bf16 (relative error 2^-9 per
+// conversion; q enters multiplied by 2^64 and p * vs by 2^62 so that the sums
+// are normal numbers, and 2^69 and 2^71 are taken out of the results. Codes, q
+// (bf16) and their products are exact. p * vs is rounded to bf16 (relative error 2^-9 per
 // term, as the bf16 cache's attention rounds p); the zero part keeps fp32 p.
 // fp32 queries and fp32 p * vs enter as three bf16 parts each (24 bits), so an
 // fp32 call keeps fp32 accuracy.
@@ -271,9 +271,17 @@ __device__ __forceinline__ void mma_row0(float& d0, float& d1, const uint32_t (&
 // A warp takes two blocks at a time (one stage of its ring): the two
 // independent chains of products and exponentials hide each other's latency,
 // and the barrier, the check of the running maximum and the loop's own
-// instructions are shared. Weights p carry a factor 2^64 throughout (in the
-// exponent, for nothing), which is what keeps products with subnormal codes
-// normal numbers.
+// instructions are shared.
+//
+// The factor 2^62 of a bf16 call's p * vs, which keeps products with subnormal
+// codes normal numbers, is put on vs (exactly), not on p: the sums of p and of
+// p * zero are plain fp32 sums, which values up to 2^60 leave far below 2^128.
+// p * vs itself is largest at p = 2^8 (the reference is moved beyond that) and
+// vs = 2^61 / 15: 2^127.1, still a bf16 number. A product is lost below
+// 2^-149, so a code part counts down to 2^-78 beside a weight of 1.
+// (With the factor in the exponent of p, 32 equal weights of values 2^59 made
+// 2^128; and m - 64 is rounded for references m beyond 2^30, which leaves
+// weights of 2^128 or 1 where 2^64 is meant.)
 //
 // Rounding p * scale to bf16 costs 2^-9 of each term p * scale * code, and the
 // codes' common part (their mean is near 8 of 15) would make that error three
@@ -292,19 +300,16 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
   constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;    // bf16 parts of q and of p * scale
   constexpr int NG = D / kKv4Group;
   constexpr int NW = kKv4Warps<T>, ST = kKv4Stages, REC = C::kRec;
-  // the weights' factor, as an exponent and as a number (fp32: none; a sum with
-  // 64 would cost the exponent's argument six bits)
-  constexpr float kOff = PARTS == 1 ? 64.f : 0.f;
-  constexpr float kUp = PARTS == 1 ? 18446744073709551616.f : 1.f;
+  constexpr float kUp = PARTS == 1 ? 4611686018427387904.f : 1.f;   // 2^62 on the value scales
   constexpr float kDown = 5.9029581035870565e+20f;              // 2^69
   constexpr uint32_t kOnes = 0x00010001u;                       // code 1 in both halves
   constexpr uint32_t kOne = PARTS == 1 ? kOnes : 0x3f803f80u, kOneHigh = PARTS == 1 ? 0x00100010u : kOne;
   constexpr float kMid = 8.f;                                   // code the products are taken about
   constexpr float kMidK = PARTS == 1 ? 0.f : 8.f;
   constexpr float kKeys = PARTS == 1 ? kDown : 1.f;             // what brings q . code back
-  // what brings the running sums back: 2^69 (and 1/16 of it where codes count
-  // 16-fold), for fp32, whose value codes are used as numbers, 2^-64
-  constexpr float kBack = PARTS == 1 ? kDown : 1.f / kUp, kRow8 = PARTS == 1 ? 0.0625f : 1.f;
+  // what brings the running sums back: 2^71 (and 1/16 of it where codes count
+  // 16-fold); nothing for fp32, whose value codes are used as numbers
+  constexpr float kBack = PARTS == 1 ? 2361183241434822606848.f : 1.f, kRow8 = PARTS == 1 ? 0.0625f : 1.f;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(8) uint64_t bars[NW][ST];
   __shared__ uint32_t s_total, s_row_start;
@@ -531,10 +536,10 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
       ones[i][0] = 0.f; ones[i][1] = 0.f;
       zo0[i] = 0.f; zo1[i] = 0.f;
     }
-    // n = kOff - m with m the reference (log2 units) of the weights 2^(s + n)
+    // n = -m with m the reference (log2 units) of the weights 2^(s + n), exactly
     // (finite: logits of minus infinity, as an overflow of fp32 leaves them,
     // weigh 0 before any other has come)
-    float n0 = 3.4e38f, n1 = 3.4e38f, l0 = 0.f, l1 = 0.f;
+    float n0 = 3.402823466e38f, n1 = 3.402823466e38f, l0 = 0.f, l1 = 0.f;
 
     int k = 0;
     for (; k < count; ++k) {
@@ -639,9 +644,9 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
         for (int e = 0; e < 4; ++e) s[u][e] = __fmul_rn(s[u][e], to_log2);
       const float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
       const float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
-      if (__any_sync(0xffffffffu, !(x0 + n0 <= kOff + 8.f && x1 + n1 <= kOff + 8.f))) {
-        const float r0 = fminf(n0, kOff - warp_max_xor(x0, 16, 4));
-        const float r1 = fminf(n1, kOff - warp_max_xor(x1, 16, 4));
+      if (__any_sync(0xffffffffu, !(x0 + n0 <= 8.f && x1 + n1 <= 8.f))) {
+        const float r0 = fminf(n0, -warp_max_xor(x0, 16, 4));
+        const float r1 = fminf(n1, -warp_max_xor(x1, 16, 4));
         const float al0 = ex2_ftz(r0 - n0), al1 = ex2_ftz(r1 - n1);
         n0 = r0; n1 = r1;
         l0 *= al0; l1 *= al1;
@@ -673,7 +678,8 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
           uint32_t pb[PARTS][2];
           float e0[PARTS], e1[PARTS], e2[PARTS], e3[PARTS];
           if constexpr (PARTS == 1) {
-            e0[0] = p0 * sa; e1[0] = p1 * sa; e2[0] = p2 * sb; e3[0] = p3 * sb;
+            const float ua = sa * kUp, ub = sb * kUp;
+            e0[0] = p0 * ua; e1[0] = p1 * ua; e2[0] = p2 * ub; e3[0] = p3 * ub;
           } else {
             bf16_parts<PARTS>(p0 * sa, e0);
             bf16_parts<PARTS>(p1 * sa, e1);
@@ -734,11 +740,6 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
         zo1[i] += __shfl_xor_sync(0xffffffffu, zo1[i], m);
       }
     }
-#pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      zo0[i] *= 1.f / kUp;
-      zo1[i] *= 1.f / kUp;
-    }
     constexpr int OR = merge_row(D);
     float* sm = reinterpret_cast<float*>(ring + C::kRing);
     float* sm_o = sm;                             // [NW][8][OR]
@@ -746,8 +747,8 @@ __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     float* sm_l = sm_m + NW * 8;
     const int h0 = 2 * cq, h1 = 2 * cq + 1;
     if (gq == 0) {
-      sm_m[warp * 8 + h0] = kOff - n0; sm_l[warp * 8 + h0] = l0 * (1.f / kUp);
-      sm_m[warp * 8 + h1] = kOff - n1; sm_l[warp * 8 + h1] = l1 * (1.f / kUp);
+      sm_m[warp * 8 + h0] = -n0; sm_l[warp * 8 + h0] = l0;
+      sm_m[warp * 8 + h1] = -n1; sm_l[warp * 8 + h1] = l1;
     }
     if (h0 < a.G) {
       // rows gq + 8 hold codes read 16 times too large

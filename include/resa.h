@@ -388,7 +388,8 @@ RESA_API int resa_evict(const resa_dims* dims, const void* k_cache, const void* 
  *      scales of token 8h + r, group g: [r][h][g][4].
  *  - Values must be finite and below 2^60 in magnitude, queries below 2^60;
  *    others give unspecified outputs in their own row (NaN and infinity are
- *    not carried through the format). softmax_scale must be below 1e17.
+ *    not carried through the format). softmax_scale must be below 1e17. A bf16
+ *    decode call's outputs are off by up to 2^-60 besides its roundings.
  *  - dims.dtype is the type of q, k, v, desc and out; the records are the same
  *    for both types.
  *  - lens is optional in these calls (NULL: every row has `len` tokens); with

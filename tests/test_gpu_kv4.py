@@ -473,3 +473,100 @@ def test_a_model_step_from_packed_prompts_to_a_4_bit_cache(resa):
             assert len(mine) == resa.num_selected(int(lt[b]), 0.3, 4) and mine[-1] == (int(lt[b]) - 1) // 16
             check(resa, qs[b:b + 1, h * G:(h + 1) * G], recs[b:b + 1, h:h + 1], [int(lt[b])], np.array([[mine]]),
                   got[b:b + 1, h * G:(h + 1) * G], gl[b:b + 1, h * G:(h + 1) * G], scale, "bf16", d, 1)
+
+
+def dense_both_ways(resa, q, k, v, n, scale, dtype):
+    """Outputs and log-sum-exp of a dense step over n quantised tokens, with and
+    without row lengths (two cuts of the work), and the records."""
+    B, H, cap, d = k.shape
+    rec = torch.zeros(B, H, cap // 16, ops.kv4_record_bytes(d), dtype=torch.uint8, device="cuda")
+    resa.kv4_quantize(dev(k, dtype), dev(v, dtype), n, rec, q.shape[1])
+    qt, res = dev(q, dtype), []
+    ws = resa.alloc_kv4_workspace(resa.dims_kv4(rec, qt), n)
+    for lens in (None, torch.full((B,), n, dtype=torch.int32, device="cuda")):
+        out, lse = torch.empty_like(qt), torch.empty(B, q.shape[1], device="cuda")
+        resa.decode_dense_kv4(qt, None, None, rec, None, n, scale, out, ws, lse=lse, lens=lens)
+        assert resa.workspace_status(ws) == resa.RESA_OK
+        res.append((out.double().cpu().numpy(), lse.double().cpu().numpy()))
+    return rec.cpu().numpy(), res
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [32, 8192])
+@pytest.mark.parametrize("ramp", [0.0, 5.0, 12.0])
+@pytest.mark.parametrize("e", [59, 55, 50, -50])
+def test_values_over_their_whole_range(resa, dtype, d, n, ramp, e):
+    """Values just below 2^60 (and far below 1): one head's first group constant,
+    the others of both signs; equal logits, and logits that grow by `ramp`, so
+    that weights pass the running reference by up to 2^8 before it moves."""
+    B, H, G = 1, 2, 4
+    k = np.zeros((B, H, n, d), np.float32)
+    k[..., 0] = ops.bf16_round(np.linspace(0, ramp, n).astype(np.float32))
+    v = ops.bf16_round(np.clip(rnd(2, B, H, n, d, dtype=dtype), -1.9, 1.9) * np.float32(2.0 ** e))
+    v[:, 0, :, :64] = 2.0 ** e
+    q = np.zeros((B, H * G, d), np.float32)
+    q[..., 0] = 1.0
+    rec, res = dense_both_ways(resa, q, k, v, n, 1.0, dtype)
+    for out, lse in res:
+        check(resa, q, rec, [n], None, out, lse, 1.0, dtype, d, H)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [3e4, 1e5, 1e6])
+def test_large_finite_logits(resa, dtype, size):
+    """Queries and keys of 1e4 to 1e6: logits far beyond 2^24, whose rounding is
+    wider than any weight's exponent. Where the largest is ahead of the next by
+    more than both may be off, the definition gives its value alone."""
+    B, H, G, d, n = 2, 2, 4, 128, 300
+    scale = 1.0 / math.sqrt(d)
+    q = ops.bf16_round(rnd(1, B, H * G, d) * np.float32(size))
+    k = ops.bf16_round(rnd(2, B, H, 304, d) * np.float32(size))
+    v = rnd(3, B, H, 304, d, dtype=dtype)
+    rec, res = dense_both_ways(resa, q, k, v, n, scale, dtype)
+    clear = 0
+    for b in range(B):
+        for g in range(H):
+            (kc, ks, kz), (vc, vs, vz) = [tuple(x[:n] for x in y) for y in ops.kv4_unpack(rec[b, g], d)]
+            kv, vv = ops.kv4_value(kc, ks, kz), ops.kv4_value(vc, vs, vz)
+            for h in range(g * G, g * G + G):
+                z = kv @ q[b, h].astype(np.float64) * scale
+                # (as in `bounds`, and the rounding to log2 units)
+                mag = (np.abs(kz) + 15 * ks).max(-1).max()
+                e = (2 * d + 16) * 2.0 ** -24 * scale * np.abs(q[b, h]).sum() * mag + 2.0 ** -22 * np.abs(z).max()
+                top = np.sort(z)[-2:]
+                for out, lse in res:
+                    assert np.isfinite(out[b, h]).all() and abs(lse[b, h] - top[1]) <= e + 6.0
+                    if top[1] - top[0] > 2 * e + 100:
+                        clear += 1
+                        want = vv[z.argmax()]
+                        # the code part's rounding, about code 8, and the output's
+                        half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -21
+                        part = 8 * np.repeat(vs[z.argmax()], 64)
+                        assert (np.abs(out[b, h] - want) <= half * 1.02 * (part + np.abs(want))).all()
+    assert clear >= B * H * G
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_equal_logits_of_any_size(resa, dtype):
+    """Heads whose logits are all equal, 2^20 to 2^40 in log2 units: the mean."""
+    B, H, G, d, n = 1, 4, 8, 64, 48
+    k = np.zeros((B, H, n, d), np.float32)
+    k[..., :] = 1024.0                                   # (constant groups are exact)
+    v = rnd(3, B, H, n, d, dtype=dtype)
+    q = np.zeros((B, H * G, d), np.float32)
+    q[0, :, 0] = ops.bf16_round((2.0 ** np.linspace(10, 30, H * G)).astype(np.float32))
+    rec, res = dense_both_ways(resa, q, k, v, n, 1.0, dtype)
+    for out, lse in res:
+        for g in range(H):
+            _, (vc, vs, vz) = [tuple(x[:n] for x in y) for y in ops.kv4_unpack(rec[0, g], d)]
+            vv = ops.kv4_value(vc, vs, vz)
+            want = vv.mean(0)
+            # weights of exactly 1 each: roundings of p * scale to bf16 (exact:
+            # the scale is bf16), of sums (32 additions) and of the output
+            half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -23
+            tol = half * np.abs(want) * 1.02 + 64 * 2.0 ** -23 * (np.abs(vz).max() + 15 * vs.max())
+            for h in range(g * G, g * G + G):
+                z = 1024.0 * float(q[0, h, 0])
+                assert (np.abs(out[0, h] - want) <= tol).all()
+                assert abs(lse[0, h] - (z + math.log(n))) <= 2.0 ** -22 * z + 2.0 ** -18
