@@ -81,6 +81,12 @@ struct PackedCfg {
   static constexpr int kRegsSoftmax = 200, kRegsOther = NT == 2 ? 104 : 56;
 };
 
+// The weights 2^(s sl2 - m) take the product unrounded and m, the largest
+// product, rounded: one factor 2^(its rounding) on the whole row, which from
+// |m| = 2^31 on fp32 does not hold. Rows beyond this bound round every product
+// before m is subtracted.
+constexpr float kFar = 16777216.f;
+
 __device__ __forceinline__ float ex2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -392,7 +398,9 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
     const int qpos_lo = q0 + w * QT;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float sl2 = a.scale_log2;
-    float m_ref = -INFINITY, l = 0.f;
+    // reference and sum of the row; the maximum beyond which the reference moves;
+    // what the weights add to s * sl2
+    float m_ref = -INFINITY, l = 0.f, limit = -INFINITY, nm = 0.f;
     bool ok = true;
     for (int t = 0; t < nt; ++t) {
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar_s[w], t & 1, a.ctrl));
@@ -432,8 +440,6 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
       // P of 64 keys (the chunks c0, c0 + 1) for the reference m_ref, over the
       // S columns they came from (all of S is in registers)
       auto weights = [&](int c0) {
-        // (a row with no visible key yet, -inf - -inf, takes weight 0)
-        const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
         const uint64_t sl2_2 = f2_pack(sl2, sl2), nm_2 = f2_pack(nm, nm);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -462,8 +468,8 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
       for (int i = 0; i < 32; ++i) mp[i & 7] = max3(mp[i & 7], s[1][i], s[3][i]);
       const float mx =
           fmaxf(max3(max3(mp[0], mp[1], mp[2]), mp[3], mp[4]), max3(mp[5], mp[6], mp[7])) * sl2;
-      const bool need = mx > m_ref + 8.f;
-      if (__any_sync(0xffffffffu, need)) {
+      if (__any_sync(0xffffffffu, mx > limit)) {
+        const bool need = mx > m_ref + 8.f;
         const float m_new = need ? mx : m_ref;
         const float alpha = need ? (m_ref == -INFINITY ? 0.f : ex2_fast(m_ref - m_new)) : 1.f;
         if (t > 0) {
@@ -481,6 +487,23 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
         }
         l *= alpha;
         m_ref = m_new;
+        // Far rows (see kFar) come here with every tile and make s relative to
+        // their reference. (A branch of its own for them, which ordinary inputs
+        // never take, costs 3 % at 32K tokens.)
+        const bool far = fabsf(m_ref) > kFar && m_ref != -INFINITY;
+        limit = far ? -INFINITY : m_ref + 8.f;
+        // (a row with no visible key yet, -inf - -inf, takes weight 0)
+        nm = far || m_ref == -INFINITY ? 0.f : -m_ref;
+        if (__any_sync(0xffffffffu, far)) {
+          const float inv = 1.f / sl2;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float rel = __fsub_rn(__fmul_rn(s[c][i], sl2), m_ref) * inv;
+              s[c][i] = far ? rel : s[c][i];
+            }
+        }
       }
       // each half of P is handed over by itself: its products run while the
       // other half's exponentials do

@@ -252,3 +252,54 @@ def test_prefill_then_decode_ragged(resa):
             ref, _, p = ops.attend_row(dq[b, h * G:(h + 1) * G], kk, vv, scale)
             tol = 2.0 ** -8 * (p @ np.abs(vv) + np.abs(ref)) * 1.02 + 1e-5
             assert (np.abs(o[b, h * G:(h + 1) * G] - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("longest", [None, 2100])
+@pytest.mark.parametrize("size", [3e4, 1e5, 1e6])
+def test_large_finite_logits(resa, longest, size):
+    """Queries and keys of 1e4 to 1e6, as the header allows: logits of 2^30 and
+    more in log2 units, whose rounding is wider than any weight's exponent.
+    Where a row's largest is ahead of the next by more than both may be off, the
+    definition gives its value alone."""
+    lens, G, d = [300, 77], 4, 128
+    st, scale = starts_of(lens), 1.0 / math.sqrt(d)
+    q, k, v = rnd(1, st[-1], G, d), rnd(2, st[-1], 1, d), rnd(3, st[-1], 1, d)
+    q, k = ops.bf16_round(q * np.float32(size)), ops.bf16_round(k * np.float32(size))
+    out, kc, vc, ds, ws, scale = call(resa, q, k, v, st, 2112, longest, scale=scale)
+    assert resa.workspace_status(ws) == resa.RESA_OK
+    o = out.double().cpu().numpy()
+    assert np.isfinite(o).all()
+    clear = 0
+    for a, b in zip(st[:-1], st[1:]):
+        n = b - a
+        for h in range(G):
+            qq, kk = q[a:b, h].astype(np.float64), k[a:b, 0].astype(np.float64)
+            z = np.where(np.tril(np.ones((n, n), bool)), qq @ kk.T * scale, -np.inf)
+            # (as in `bounds`, and the rounding to log2 units)
+            e = (2 * d + 16) * 2.0 ** -24 * scale * np.abs(qq).sum(-1) * np.abs(kk).max()
+            e = e + 2.0 ** -22 * np.abs(z[np.isfinite(z)]).max()
+            top = np.sort(z, -1)[:, -2:]
+            gap = np.full(n, np.inf)
+            gap[1:] = top[1:, 1] - top[1:, 0]
+            for i in np.flatnonzero(gap > 2 * e + 100):
+                clear += 1
+                want = v[a + z[i].argmax(), 0].astype(np.float64)
+                assert (np.abs(o[a + i, h] - want) <= 2.0 ** -8 * 2.02 * np.abs(want)).all(), (a + i, h)
+    assert clear > st[-1] * G // 2
+
+
+@pytest.mark.parametrize("longest", [None, 2100])
+def test_equal_logits_of_any_size(resa, longest):
+    """Heads whose logits are all equal, +-2^20 to 2^40 in log2 units: the running mean."""
+    n, G, d = 140, 8, 64
+    q, k, v = np.zeros((n, G, d), np.float32), np.zeros((n, 1, d), np.float32), rnd(3, n, 1, d)
+    q[:, :, 0] = ops.bf16_round((2.0 ** np.linspace(10, 30, G) * np.array([1, -1] * (G // 2))).astype(np.float32))
+    k[:, :, 0] = 1024.0
+    out, kc, vc, ds, ws, scale = call(resa, q, k, v, [0, n], 2112, longest, scale=1.0)
+    o = out.double().cpu().numpy()
+    want = np.cumsum(v[:, 0].astype(np.float64), 0) / np.arange(1, n + 1)[:, None]
+    # weights of one size each, so that their rounding to bf16 is one factor of
+    # all of them (up to 2^-8); sums of n terms; the output's rounding
+    tol = 2.0 ** -8 * 2.02 * np.abs(want) + n * 2.0 ** -23 * np.abs(v).max()
+    for h in range(G):
+        assert (np.abs(o[:, h] - want) <= tol).all(), h
