@@ -57,6 +57,12 @@ struct RectK {
   float scale_log2;
 };
 
+// The weights 2^(s sl2 - m) take the product unrounded and m, the largest
+// product, rounded: one factor 2^(its rounding) on the whole row, which from
+// |m| = 2^31 on fp32 does not hold. Rows beyond this bound round every product
+// before m is subtracted.
+constexpr float kFar = 16777216.f;
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -271,7 +277,9 @@ __global__ void __launch_bounds__(288, 1) rectify_tc_kernel(const __grid_constan
     const int64_t qpos = len - win + qi;                   // causal limit of this row
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float sl2 = a.scale_log2;
-    float m_ref = -INFINITY, l = 0.f;                      // reference max (log2 units), sum
+    // reference max (log2 units) and sum; the maximum beyond which the reference
+    // moves; what the weights add to s * sl2
+    float m_ref = -INFINITY, l = 0.f, limit = -INFINITY, nm = 0.f;
     bool ok = true;
     int u = 0;
     for (int t = w; t < nt; t += 2, ++u) {
@@ -316,8 +324,8 @@ __global__ void __launch_bounds__(288, 1) rectify_tc_kernel(const __grid_constan
         tc::fence_after_sync();
       }
       // move the reference only when the row maximum grew by more than 2^8
-      const bool need = mx > m_ref + 8.f;
-      if (__any_sync(0xffffffffu, need)) {
+      if (__any_sync(0xffffffffu, mx > limit)) {
+        const bool need = mx > m_ref + 8.f;
         const float m_new = need ? mx : m_ref;
         const float alpha = need ? (m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new)) : 1.f;
         if (u > 0) {
@@ -334,12 +342,32 @@ __global__ void __launch_bounds__(288, 1) rectify_tc_kernel(const __grid_constan
         }
         l *= alpha;
         m_ref = m_new;
+        // Far rows (see kFar) come here with every tile and make their S
+        // relative to the reference.
+        const bool far = fabsf(m_ref) > kFar && m_ref != -INFINITY;
+        limit = far ? -INFINITY : m_ref + 8.f;
+        nm = far || m_ref == -INFINITY ? 0.f : -m_ref;
+        if (__any_sync(0xffffffffu, far)) {
+          const float inv = 1.f / sl2;
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            float x[32];
+            tc::ld32(tS(w) + lane_off + c4 * 32, x);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float rel = __fsub_rn(__fmul_rn(x[i], sl2), m_ref) * inv;
+              x[i] = far ? rel : x[i];
+            }
+            tc::st32(tS(w) + lane_off + c4 * 32, x);
+          }
+          tc::wait_st();
+        }
       }
       // pass 2: P = 2^(s * scale - m_ref) as bf16 pairs into TMEM columns
       // 16 c4 .. 16 c4 + 15 of S (keys 32 c4 .. 32 c4 + 31): below the columns
       // still to be read, above none the A operand needs later
       const bool live = m_ref != -INFINITY;
-      const float nm = live ? -m_ref : 0.f;
       float sum = 0.f;
 #pragma unroll
       for (int c4 = 0; c4 < 4; ++c4) {
