@@ -39,6 +39,14 @@ __device__ __forceinline__ bool row_skipped(const AttnK& a, int b, int r) {
   return r >= w || row_len(a.lens, a.len0 + a.R - 1, b) < w;
 }
 
+// A dense step has no score kernel, which reports a row length out of range:
+// one thread per batch row does it here.
+__device__ __forceinline__ void report_len(const AttnK& a, int s_idx, int g, int b) {
+  if (a.sel == nullptr && a.lens != nullptr && s_idx == 0 && g == 0 && threadIdx.x == 0 &&
+      row_len_bad(a.lens, a.len0 + a.R - 1, b))
+    raise_error(a.ctrl, kErrBadIndex);
+}
+
 constexpr int kIdCache = 1024;   // block ids of one CTA kept in shared memory
 
 __device__ __forceinline__ void split_range(const AttnK& a, int s, int64_t len_r, int& i0,
@@ -109,6 +117,7 @@ __global__ void __launch_bounds__(NW * 32) attend_bf16_kernel(const __grid_const
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (row_skipped(a, b, r)) return;
   const int64_t len_r = query_len(a, b, r);
+  report_len(a, s_idx, g, b);
   int i0, i1;
   split_range(a, s_idx, len_r, i0, i1);
   const int span = i1 - i0;
@@ -172,6 +181,7 @@ __global__ void __launch_bounds__(NW * 32) attend_f32_kernel(AttnK a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (row_skipped(a, b, r)) return;
   const int64_t len_r = query_len(a, b, r);
+  report_len(a, s_idx, g, b);
   const float* qrow = static_cast<const float*>(a.q) + (static_cast<int64_t>(br) * a.Hq + g * a.G) * D;
   for (int i = threadIdx.x; i < a.G * D; i += NW * 32) sq[i] = qrow[i];
   __syncthreads();
@@ -326,6 +336,7 @@ __global__ void __launch_bounds__(NW * 32) attend_f32_keep_kernel(AttnK a) {
   issue(0);
   issue(1);
   issue(2);
+  report_len(a, s_idx, g, b);
   const float* qg = static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.Hq + g * a.G) * D;
   for (int i = threadIdx.x; i < a.G * D; i += NW * 32) sq[i] = qg[i];
   __syncthreads();

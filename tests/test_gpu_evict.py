@@ -330,3 +330,29 @@ def test_captured_step_and_eviction(resa):
     for x, y in zip(a[2:3] + a[4:], e[2:3] + e[4:]):
         assert torch.equal(x, y)
     assert resa.workspace_status(a[3]) == resa.RESA_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("form", ["weights", "dense"])
+def test_length_out_of_range_is_clamped_and_flagged(resa, dtype, form):
+    """A dense step with row lengths of 0 and beyond the bound does what it does
+    at the nearest lengths allowed, and reports them."""
+    B, H, G, d, n = 3, 2, 2, 64, 100
+    k, v = rnd(1, B, H, 112, d, dtype=dtype), rnd(2, B, H, 112, d, dtype=dtype)
+    q, kn, vn = (dev(rnd(3 + i, B, x, d, dtype=dtype), dtype) for i, x in enumerate((H * G, H, H)))
+    res = []
+    for lens, want in (([0, 50, 101], resa.RESA_ERR_BAD_INDEX), ([1, 50, 100], resa.RESA_OK),
+                       ([-7, 50, 100], resa.RESA_ERR_BAD_INDEX)):
+        kt, vt = dev(k, dtype), dev(v, dtype)
+        desc = torch.zeros(B, H, 7, 2, d, dtype=DT[dtype], device="cuda")
+        w, out = torch.ones(B, H, 112, device="cuda"), torch.empty_like(q)
+        ws = resa.alloc_weights_workspace(resa.dims_for(kt, H * G), n)
+        lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        if form == "weights":
+            resa.decode_dense_weights(q, kn, vn, kt, vt, desc, w, n, 0.125, out, None, ws, lens=lt)
+        else:
+            resa.decode_dense_varlen(q, kn, vn, kt, vt, desc, lt, n, 0.125, out, ws)
+        assert resa.workspace_status(ws) == want, lens
+        res.append((out, kt, vt, desc, w))
+    for other in (res[0], res[2]):
+        assert all(torch.equal(x, y) for x, y in zip(res[1], other))
