@@ -81,6 +81,33 @@ struct PackedCfg {
   static constexpr int kRegsSoftmax = 200, kRegsOther = NT == 2 ? 104 : 56;
 };
 
+// The ring: copy n (K of tile n / 2 where n is even, V where it is odd) goes to
+// slot n % slots. The slot's last tile, copy n - slots, is given back with the
+// one before or after it: K 0 alone first (give-back 0), then V t and K t + 1
+// together (give-back t + 1). Which give-back copy n waits for, -1 for none:
+__host__ __device__ constexpr int packed_waits_for(int n, int slots) {
+  return n >= slots && (n == slots || (n - slots) % 2 == 1) ? (n - slots + 1) / 2 : -1;
+}
+// and how many of them the copies of n_tiles tiles wait for. No other is made:
+// its arrival could reach a barrier of a CTA that has ended.
+__host__ __device__ constexpr int packed_give_backs(int n_tiles, int slots) {
+  return 2 * n_tiles > slots ? (2 * n_tiles - slots) / 2 + 1 : 0;
+}
+constexpr bool packed_ring_agrees(int slots) {
+  for (int tiles = 1; tiles < 40; ++tiles) {
+    int next = 0;
+    for (int n = 0; n < 2 * tiles; ++n) {
+      const int f = packed_waits_for(n, slots);
+      if (f >= 0 && f != next++) return false;
+      // the give-back that frees the slot is waited for by then
+      if (n >= slots && (n - slots + 1) / 2 >= next) return false;
+    }
+    if (next != packed_give_backs(tiles, slots)) return false;
+  }
+  return true;
+}
+static_assert(packed_ring_agrees(2) && packed_ring_agrees(5), "ring of K and V tiles");
+
 // The weights 2^(s sl2 - m) take the product unrounded and m, the largest
 // product, rounded: one factor 2^(its rounding) on the whole row, which from
 // |m| = 2^31 on fp32 does not hold. Rows beyond this bound round every product
@@ -288,12 +315,8 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
         bool ok = true;
         for (; n < 2 * n_tiles; ++n) {
           const int i = n % C::kSlots;
-          if (n >= C::kSlots && (n == C::kSlots || (n - C::kSlots) % 2 == 1)) {
-            // the slot's last tile, copy n - kSlots, is given back with the one
-            // before or after it: K 0 alone first, then V t and K t + 1 together
-            const int f = (n - C::kSlots + 1) / 2;
-            if (!(ok = mbar_wait_bounded(&bar_free[f % 3], (f / 3) & 1, a.ctrl))) break;
-          }
+          const int f = packed_waits_for(n, C::kSlots);
+          if (f >= 0 && !(ok = mbar_wait_bounded(&bar_free[f % 3], (f / 3) & 1, a.ctrl))) break;
           mbar_arrive_expect_tx(&bar_full[i], C::kTileBytes);
           const CUtensorMap* map = n & 1 ? &tmV : &tmK;
 #pragma unroll
@@ -345,7 +368,8 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
           tc::fence_after_sync();
           qk(w, 0);
         }
-        if (ok) tc::commit(&bar_free[0]);
+        const int backs = packed_give_backs(n_tiles, C::kSlots);
+        if (ok && backs > 0) tc::commit(&bar_free[0]);
         uint32_t f = 1;                              // give-back t + 1 on barrier f
         uint32_t i = 1, ph = 0;                      // slot and phase of V of tile t
         for (int t = 0; ok && t < n_tiles; ++t) {
@@ -376,7 +400,7 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
           }
           if (!ok) break;
           // both tiles have taken V of tile t and K of tile t + 1
-          tc::commit(&bar_free[f]);
+          if (t + 1 < backs) tc::commit(&bar_free[f]);
           if (++f == 3) f = 0;
           i = i2 + 1;
           ph = ph2;
