@@ -341,14 +341,14 @@ def prefill(q, k_cache, v_cache, desc, length: int, softmax_scale: float, out, w
 def _ptrs(*tensors) -> list:
     """Addresses of the tensors (None stays None), which have to be contiguous
     and on the current CUDA device."""
-    out, dev = [], -1
+    out, dev = [], None
     for t in tensors:
         if t is None:
             out.append(None)
             continue
         at = t.get_device()                       # -1: not a CUDA tensor
         if at != dev:
-            if at < 0 or dev >= 0 or at != torch._C._cuda_getDevice():
+            if at < 0 or dev is not None or at != torch._C._cuda_getDevice():
                 raise ValueError("tensors must be on the current CUDA device")
             dev = at
         if not t.is_contiguous():

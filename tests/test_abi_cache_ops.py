@@ -201,3 +201,28 @@ def test_binding_refuses_what_the_library_cannot_see(resa):
     with pytest.raises(ValueError):
         resa.evict(k, k, torch.zeros(1, 2, 48), 10, 5, 1, torch.zeros(1, 2, 16, 32), k, None, None,
                    torch.zeros(1, 2, 5, dtype=torch.int32), 4, ws)
+
+
+def test_tensors_of_the_cpu_are_refused(resa):
+    """No address of host memory reaches a kernel, whether all tensors of a call
+    or some of them lie there."""
+    def z(*shape, dtype=torch.float32):
+        return torch.zeros(shape, dtype=dtype)
+
+    q, k, ws = z(1, 4, 64), z(1, 2, 48, 64), z(1 << 20, dtype=torch.uint8)
+    kv4, lens = z(1, 2, 3, 1152, dtype=torch.uint8), z(1, dtype=torch.int32)
+    sel, w = z(1, 2, 2, dtype=torch.int32), z(1, 2, 48)
+    calls = [lambda: resa._ptrs(q), lambda: resa._ptrs(None, q, k),
+             lambda: resa.kv4_quantize(k, k, 10, kv4, 4),
+             lambda: resa.kv4_dequantize(kv4, 10, k, k, 4, lens=lens),
+             lambda: resa.decode_dense_kv4(q, None, None, kv4, None, 10, 1.0, z(1, 4, 64), ws),
+             lambda: resa.decode_sparse_kv4(q, None, None, kv4, z(1, 2, 3, 2, 64), 48, 0.5, 1, 1.0, z(1, 4, 64), ws),
+             lambda: resa.attend_blocks_kv4(q, kv4, 48, sel, 1.0, z(1, 4, 64), ws),
+             lambda: resa.decode_dense_weights(q, None, None, k, k, None, w, 10, 1.0, z(1, 4, 64), None, ws),
+             lambda: resa.evict(k, k, w, 10, 5, 1, z(1, 2, 16, 64), z(1, 2, 16, 64), None, None,
+                                z(1, 2, 5, dtype=torch.int32), 4, ws),
+             lambda: resa.prefill_packed(z(9, 4, 64), z(9, 2, 64), z(9, 2, 64), z(2, dtype=torch.int32), 9, k, k, None,
+                                         1.0, z(9, 4, 64), ws)]
+    for f in calls:
+        with pytest.raises(ValueError, match="CUDA device"):
+            f()
