@@ -389,16 +389,28 @@ def prefill_packed(q, k, v, starts, longest: int, k_cache, v_cache, desc, softma
                    out, workspace, stream=None) -> None:
     """Causal attention over packed prompts (q, out: [total, Hq, d]; k, v:
     [total, Hkv, d]; starts: int32 CUDA tensor [batch + 1]), which also fills
-    rows of k_cache and v_cache [batch, Hkv, max_len, d] and desc (or None)."""
-    B, H, L, d = k_cache.shape
-    T, Hq, dq = q.shape
-    if (k.shape != (T, H, d) or v.shape != k.shape or out.shape != q.shape
-            or k_cache.shape != v_cache.shape or dq != d):
-        raise ValueError("q, out must be [total, n_q_heads, d] and k, v [total, n_kv_heads, d]")
-    if any(t.dtype != k_cache.dtype for t in (q, k, v, v_cache, out)):
-        raise ValueError("q, k, v, out and the caches must share a dtype")
-    if starts.dtype != torch.int32 or starts.shape != (B + 1,):
+    rows of k_cache and v_cache [batch, Hkv, max_len, d] (both or neither None)
+    and desc (or None)."""
+    if (k_cache is None) != (v_cache is None):
+        raise ValueError("k_cache and v_cache: both or neither")
+    if starts.dtype != torch.int32 or starts.dim() != 1 or starts.numel() < 2:
         raise ValueError("starts must be int32 [batch + 1]")
+    B = starts.numel() - 1
+    T, Hq, d = q.shape
+    H = k.shape[1]
+    # without a cache the capacity only sizes desc, or bounds `longest`
+    if k_cache is not None:
+        L = k_cache.shape[2]
+    else:
+        L = -(-max(int(longest), 1) // BLOCK) * BLOCK
+        if desc is not None and desc.dim() == 5:
+            L = desc.shape[2] * BLOCK
+    if k.shape != (T, H, d) or v.shape != k.shape or out.shape != q.shape:
+        raise ValueError("q, out must be [total, n_q_heads, d] and k, v [total, n_kv_heads, d]")
+    if k_cache is not None and (k_cache.shape != (B, H, L, d) or v_cache.shape != k_cache.shape):
+        raise ValueError("the caches must be [batch, n_kv_heads, max_len, d]")
+    if any(t is not None and t.dtype != q.dtype for t in (k, v, out, k_cache, v_cache)):
+        raise ValueError("q, k, v, out and the caches must share a dtype")
     if desc is not None and (desc.shape != (B, H, L // BLOCK, 2, d) or desc.dtype != q.dtype):
         raise ValueError("desc must be [batch, n_kv_heads, max_len / 16, 2, head_dim]")
     pq, pk, pv, ps, pkc, pvc, pd, po, pw = _ptrs(q, k, v, starts, k_cache, v_cache, desc, out,

@@ -226,3 +226,16 @@ def test_tensors_of_the_cpu_are_refused(resa):
     for f in calls:
         with pytest.raises(ValueError, match="CUDA device"):
             f()
+
+
+def test_packed_prompts_without_caches_are_checked_like_others(resa):
+    """Caches may be left out (both); what is left is checked all the same."""
+    q, k, st = torch.zeros(9, 4, 64), torch.zeros(9, 2, 64), torch.zeros(3, dtype=torch.int32)
+    c, desc, ws = torch.zeros(2, 2, 16, 64), torch.zeros(2, 2, 1, 2, 64), torch.zeros(1024, dtype=torch.uint8)
+    for kw, what in ((dict(), "CUDA"), (dict(ds=None), "CUDA"), (dict(kc=c, vc=c), "CUDA"),
+                     (dict(kc=c), "both"), (dict(vc=c), "both"), (dict(ds=desc[:1]), "desc"), (dict(ds=desc[0]), "desc"),
+                     (dict(kc=c[:1], vc=c[:1]), "caches"), (dict(kc=c, vc=c.bfloat16()), "dtype"),
+                     (dict(st=st[:1]), "starts"), (dict(st=st.long()), "starts"), (dict(k=k[:8]), "total")):
+        a = dict(dict(k=k, st=st, kc=None, vc=None, ds=desc), **kw)
+        with pytest.raises(ValueError, match=what):
+            resa.prefill_packed(q, a["k"], k, a["st"], 9, a["kc"], a["vc"], a["ds"], 1.0, torch.zeros_like(q), ws)

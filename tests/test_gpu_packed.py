@@ -303,3 +303,25 @@ def test_equal_logits_of_any_size(resa, longest):
     tol = 2.0 ** -8 * 2.02 * np.abs(want) + n * 2.0 ** -23 * np.abs(v).max()
     for h in range(G):
         assert (np.abs(o[:, h] - want) <= tol).all(), h
+
+
+@pytest.mark.parametrize("longest", [None, 2100])
+@pytest.mark.parametrize("desc", [True, False])
+def test_without_caches(resa, longest, desc):
+    """Caches left out: the same outputs and descriptors, bit for bit."""
+    lens, H, G, d = [200, 0, 77, 16], 2, 4, 128
+    st = starts_of(lens)
+    q, k, v = rnd(1, st[-1], H * G, d), rnd(2, st[-1], H, d), rnd(3, st[-1], H, d)
+    cap = 208 if longest is None else 2112
+    want, kc, _, ds, ws, scale = call(resa, q, k, v, st, cap, longest)
+    out, d2 = torch.full_like(want, 9.0), torch.full_like(ds, 7.0) if desc else None
+    resa.prefill_packed(dev(q), dev(k), dev(v), torch.tensor(st, dtype=torch.int32, device="cuda"),
+                        longest or max(lens), None, None, d2, scale, out, ws)
+    assert resa.workspace_status(ws) == resa.RESA_OK
+    assert torch.equal(out, want) and (d2 is None or torch.equal(d2, ds))
+    # and a bound that the descriptors have no room for is refused
+    if desc:
+        with pytest.raises(resa.ResaError) as e:
+            resa.prefill_packed(dev(q), dev(k), dev(v), torch.tensor(st, dtype=torch.int32, device="cuda"),
+                                cap + 1, None, None, d2, scale, out, ws)
+        assert e.value.status == resa.RESA_ERR_CAPACITY
