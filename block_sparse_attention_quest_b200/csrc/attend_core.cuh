@@ -326,11 +326,8 @@ __device__ __forceinline__ bool stream_bf16(const CUtensorMap* tmK, const CUtens
     mx0 = warp_max_xor(mx0, 16, 4);
     mx1 = warp_max_xor(mx1, 16, 4);
     const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-    float r0 = mn0, r1 = mn1;
-    if constexpr (kKeep) {                       // logits so far all minus infinity: weights 0
-      r0 = mn0 == -INFINITY ? 0.f : mn0;
-      r1 = mn1 == -INFINITY ? 0.f : mn1;
-    }
+    // (logits so far all minus infinity, as an overflow leaves them: weights 0)
+    const float r0 = mn0 == -INFINITY ? 0.f : mn0, r1 = mn1 == -INFINITY ? 0.f : mn1;
     const float al0 = exp2f(m0 - r0), al1 = exp2f(m1 - r1);
     const float p0 = exp2f(s0 - r0), p2 = exp2f(s2 - r0);
     const float p1 = exp2f(s1 - r1), p3 = exp2f(s3 - r1);

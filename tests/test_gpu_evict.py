@@ -356,3 +356,25 @@ def test_length_out_of_range_is_clamped_and_flagged(resa, dtype, form):
         res.append((out, kt, vt, desc, w))
     for other in (res[0], res[2]):
         assert all(torch.equal(x, y) for x, y in zip(res[1], other))
+
+
+def test_the_plain_step_also_weighs_such_logits_with_nothing(resa):
+    """The step that keeps weights gives resa_decode_dense's outputs bit for bit,
+    also where a warp's first logits all overflow to minus infinity; and so does
+    the list of all blocks, in its own cut of the work."""
+    B, H, G, d, n, scale = 1, 2, 4, 128, 64, 1.0 / math.sqrt(128)
+    k, v, q = rnd(1, B, H, n, d), rnd(2, B, H, n, d), rnd(3, B, H * G, d)
+    k[..., 0] = 0.0
+    k[:, :, :32, 0], q[:, :, 0] = ops.bf16_round(np.float32(-1e22)), ops.bf16_round(np.float32(1e18))
+    kt, vt, qt = dev(k, "bf16"), dev(v, "bf16"), dev(q, "bf16")
+    outs = [torch.empty_like(qt) for _ in range(3)]
+    lses = [torch.empty(B, H * G, device="cuda") for _ in range(3)]
+    ws = resa.alloc_weights_workspace(resa.dims_for(kt, H * G), n)
+    resa.decode_dense_weights(qt, None, None, kt, vt, None, torch.zeros(B, H, n, device="cuda"), n, scale, outs[0],
+                              lses[0], ws)
+    resa.decode_dense(qt, None, None, kt, vt, None, n, scale, outs[1], ws, lse=lses[1])
+    sel = torch.arange(n // 16, dtype=torch.int32, device="cuda").expand(B, H, -1).contiguous()
+    resa.attend_blocks(qt, kt, vt, n, sel, scale, outs[2], ws, lse=lses[2])
+    assert resa.workspace_status(ws) == resa.RESA_OK
+    assert torch.equal(outs[0], outs[1]) and torch.equal(lses[0], lses[1])
+    assert torch.equal(outs[0], outs[2]) and bool(torch.isfinite(outs[0]).all())
