@@ -312,6 +312,8 @@ int resa_build_desc(const resa_dims* dims, const void* k_cache, int64_t len, voi
   return build_desc_impl(dims, k_cache, len, desc, stream, nullptr);
 }
 
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 static bool lens_ok(const int32_t* lens) {
   return lens != nullptr && (reinterpret_cast<uintptr_t>(lens) & 3u) == 0;
 }
@@ -697,7 +699,7 @@ int resa_decode_dense_weights(const resa_dims* dims, const void* q, const void* 
                                workspace_bytes, 0);
   if (rc != RESA_OK) return rc;
   if (!weights || !aligned16(weights) || (desc && !aligned16(desc)) || (lens && !lens_ok(lens)) ||
-      !(std::isfinite(softmax_scale) && softmax_scale > 0.f))
+      !aligned4(lse) || !(std::isfinite(softmax_scale) && softmax_scale > 0.f))
     return RESA_ERR_INVALID_ARG;
   const WeightsLayout wl = weights_layout(s, len);
   if (workspace_bytes < wl.total) return RESA_ERR_WORKSPACE;
@@ -818,13 +820,15 @@ int resa_kv4_dequantize(const resa_dims* dims, const void* kv4, int64_t len, con
 static int check_kv4_decode(const resa_dims* dims, Shape* s, const void* q, const void* k_new,
                             const void* v_new, const void* kv4, const void* desc, int64_t len,
                             const int32_t* lens, float softmax_scale, const void* out,
-                            const void* workspace, size_t workspace_bytes) {
+                            const float* lse, const int32_t* sel, const void* workspace,
+                            size_t workspace_bytes) {
   const int rc = check_dims(dims, s);
   if (rc != RESA_OK) return rc;
   if (!q || !kv4 || !out || !workspace || (k_new == nullptr) != (v_new == nullptr) ||
       !aligned16(q) || !aligned16(kv4) || !aligned16(out) || (desc && !aligned16(desc)) ||
       (k_new && (!aligned16(k_new) || !aligned16(v_new))) ||
       (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 || (lens && !lens_ok(lens)) ||
+      !aligned4(lse) || !aligned4(sel) ||
       len < 1 || !(softmax_scale > 0.f && softmax_scale < 1e17f))   // (its product with 2^69 is finite)
     return RESA_ERR_INVALID_ARG;
   if (len > s->L_max) return RESA_ERR_CAPACITY;
@@ -855,7 +859,7 @@ int resa_attend_blocks_kv4(const resa_dims* dims, const void* q, const void* kv4
                            float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   Shape s;
   const int rc = check_kv4_decode(dims, &s, q, nullptr, nullptr, kv4, nullptr, len, nullptr,
-                                  softmax_scale, out, workspace, workspace_bytes);
+                                  softmax_scale, out, lse, sel, workspace, workspace_bytes);
   if (rc != RESA_OK) return rc;
   if (!sel || n_sel < 1 || n_sel > blocks_of(len)) return RESA_ERR_INVALID_ARG;
   const int num_sms = device_sms();
@@ -871,7 +875,7 @@ int resa_decode_dense_kv4(const resa_dims* dims, const void* q, const void* k_ne
                           void* workspace, size_t workspace_bytes, void* stream) {
   Shape s;
   const int rc = check_kv4_decode(dims, &s, q, k_new, v_new, kv4, desc, len, lens, softmax_scale,
-                                  out, workspace, workspace_bytes);
+                                  out, lse, nullptr, workspace, workspace_bytes);
   if (rc != RESA_OK) return rc;
   const int num_sms = device_sms();
   if (num_sms <= 0) return RESA_ERR_CUDA;
@@ -890,7 +894,7 @@ int resa_decode_sparse_kv4(const resa_dims* dims, const void* q, const void* k_n
                            size_t workspace_bytes, void* stream) {
   Shape s;
   const int rc = check_kv4_decode(dims, &s, q, k_new, v_new, kv4, desc, len, lens, softmax_scale,
-                                  out, workspace, workspace_bytes);
+                                  out, lse, sel, workspace, workspace_bytes);
   if (rc != RESA_OK) return rc;
   if (!desc || !(r > 0.0 && r <= 1.0) || n_min < 1) return RESA_ERR_INVALID_ARG;
   if (blocks_of(len) > 262144) return RESA_ERR_UNSUPPORTED;

@@ -239,3 +239,19 @@ def test_packed_prompts_without_caches_are_checked_like_others(resa):
         a = dict(dict(k=k, st=st, kc=None, vc=None, ds=desc), **kw)
         with pytest.raises(ValueError, match=what):
             resa.prefill_packed(q, a["k"], k, a["st"], 9, a["kc"], a["vc"], a["ds"], 1.0, torch.zeros_like(q), ws)
+
+
+def test_misaligned_results_are_refused(resa):
+    """lse and sel are written (sel also read) four bytes at a time. (The
+    workspace is too small throughout: no call gets as far as a launch.)"""
+    E = resa
+    for f in ("dense", "sparse", "blocks"):
+        assert kv4_call(resa, f, lse=at(6) + 2, wsb=64) == E.RESA_ERR_INVALID_ARG, f
+        assert kv4_call(resa, f, lse=at(6) + 4, wsb=64) == E.RESA_ERR_WORKSPACE, f
+    for f in ("sparse", "blocks"):
+        assert kv4_call(resa, f, sel=at(4) + 1, wsb=64) == E.RESA_ERR_INVALID_ARG, f
+    d, small = ctypes.byref(dims(resa)), resa.workspace_bytes(dims(resa), 100)
+    for lse, want in ((at(6) + 2, E.RESA_ERR_INVALID_ARG), (at(6) + 4, E.RESA_ERR_WORKSPACE)):
+        rc = resa._lib.resa_decode_dense_weights(d, at(0), None, None, at(1), at(2), None, at(3), 100, None, 1.0, at(4),
+                                                 lse, at(5), small, None)
+        assert rc == want
