@@ -378,3 +378,57 @@ def test_the_plain_step_also_weighs_such_logits_with_nothing(resa):
     assert resa.workspace_status(ws) == resa.RESA_OK
     assert torch.equal(outs[0], outs[1]) and torch.equal(lses[0], lses[1])
     assert torch.equal(outs[0], outs[2]) and bool(torch.isfinite(outs[0]).all())
+
+
+def test_steps_evictions_and_prompts_at_once(resa):
+    """Two streams (given explicitly), a workspace each: packed prompts, steps
+    that keep weights and evictions of one stream between those of the other
+    give bit for bit what they give alone."""
+    B, H, G, d, cap, n = 2, 2, 4, 128, 4112, 4100
+    k, v = dev(rnd(1, B, H, cap, d), "bf16"), dev(rnd(2, B, H, cap, d), "bf16")
+    q, kn, vn = (dev(rnd(3 + i, B, x, d), "bf16") for i, x in enumerate((H * G, H, H)))
+    T = 3000
+    pq, pk, pv = (dev(rnd(6 + i, T, x, d), "bf16") for i, x in enumerate((H * G, H, H)))
+    dims, scale = resa.dims_for(k, H * G), 1.0 / math.sqrt(d)
+
+    class Job:
+        def __init__(self, longest):
+            self.longest = longest                   # (one query tile per CTA, or two)
+            self.k, self.v, self.w = k.clone(), v.clone(), torch.zeros(B, H, cap, device="cuda")
+            self.ws = resa.alloc_weights_workspace(dims, cap)
+            self.out, self.lse = torch.zeros_like(q), torch.zeros(B, H * G, device="cuda")
+            self.ko, self.vo = (torch.zeros(B, H, 512, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+            self.kept = torch.zeros(B, H, 500, dtype=torch.int32, device="cuda")
+            self.pout = torch.zeros_like(pq)
+            self.pk, self.pv = torch.zeros_like(k), torch.zeros_like(v)
+            self.desc = torch.zeros(B, H, cap // 16, 2, d, dtype=torch.bfloat16, device="cuda")
+            self.starts = torch.tensor([0, 1100, T], dtype=torch.int32, device="cuda")
+
+        def run(self, stream):
+            resa.prefill_packed(pq, pk, pv, self.starts, self.longest, self.pk, self.pv, self.desc, scale, self.pout,
+                                self.ws, stream=stream)
+            for _ in range(2):
+                resa.decode_dense_weights(q, kn, vn, self.k, self.v, None, self.w, n, scale, self.out, self.lse,
+                                          self.ws, stream=stream)
+            resa.evict(self.k, self.v, self.w, n, 500, 60, self.ko, self.vo, None, None, self.kept, H * G, self.ws,
+                       stream=stream)
+
+        def results(self):
+            return [self.w, self.out, self.lse, self.ko, self.vo, self.kept, self.pout, self.pk, self.pv, self.desc]
+
+    alone = []
+    for longest in (2000, 4096):
+        alone.append(Job(longest))
+        for _ in range(5):
+            alone[-1].run(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+    jobs, streams = [Job(2000), Job(4096)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for job, st in zip(jobs, streams):
+            job.run(st)
+    torch.cuda.synchronize()
+    for job, one in zip(jobs, alone):
+        assert resa.workspace_status(job.ws) == resa.RESA_OK
+        for x, y in zip(job.results(), one.results()):
+            assert torch.equal(x, y)
