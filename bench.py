@@ -50,10 +50,10 @@ METRIC = "ReSA decode-step us & achieved HBM GB/s vs roofline at 128K/256K; rect
 #     rectify_tc_kernel at 128K, f = 32 (--set full, one cold launch).
 NCU_COUNTERS = {
     "attention": {"files": ["attend.cu", "attend_core.cuh", "common.cuh", "launch.h"],
-                  "source": "a5d57e97488fbfaf",
-                  "traffic": {"resa_decode_128k_b1": 53942016}},
-    "rectify": {"files": ["rectify_tc.cu", "tc.cuh", "common.cuh", "launch.h"], "source": "2bf9fdade30738eb",
-                "tensor_pipe_active_pct": 36.22, "traffic": 541861888},
+                  "source": "bcc8e62e8fbdced8",
+                  "traffic": {"resa_decode_128k_b1": 53946240}},
+    "rectify": {"files": ["rectify_tc.cu", "tc.cuh", "common.cuh", "launch.h"], "source": "cf19d35e0bb4c510",
+                "tensor_pipe_active_pct": 36.12, "traffic": 541956352},
 }
 
 

@@ -275,7 +275,8 @@ def noalloc_status(stream=None) -> int:
 
 
 def workspace_status(workspace, stream=None) -> int:
-    """Synchronise and read (and clear) the device error flag of a workspace."""
+    """Synchronise and read (and clear) the device error flag of a workspace.
+    After an error the workspace has to be zeroed before its next use."""
     return _lib.resa_workspace_status(_ptr(workspace), _stream(stream))
 
 

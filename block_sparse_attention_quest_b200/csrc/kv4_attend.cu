@@ -29,10 +29,10 @@
 // its own ring in shared memory; the copies of a CTA's next piece are under
 // way while the warps' results of the last one are merged.
 //
-// Measured (B200, 32/8 heads, d = 128, bf16): a 128K context 35.0 us (151 MB, 0.66
+// Measured (B200, 32/8 heads, d = 128, bf16): a 128K context 34.7 us (151 MB, 0.67
 // of the copy rate), of which about 27 streaming and 8 before the first
-// product and in the merges; 1639 of 16384 blocks of a 256K context 14.1 us;
-// 16 rows of 1K to 32K tokens 66.4 us (0.70). While it streams it is bound by
+// product and in the merges; 1639 of 16384 blocks of a 256K context 14.2 us;
+// 16 rows of 1K to 32K tokens 66.7 us (0.69). While it streams it is bound by
 // instruction latency: 277 instructions per block and warp, three warps per
 // scheduler at 168 registers (sixteen warps at 128 spill and are slower).
 #include "kv4.cuh"
@@ -292,7 +292,8 @@ __device__ __forceinline__ void mma_row0(float& d0, float& d1, const uint32_t (&
 // without, 2.4e-3 with it, 1.7e-3 being the output's own rounding.) An fp32
 // call makes bf16 numbers of code - 8 instead, for keys too, so that its sums
 // stay small and of both signs: the tensor cores truncate, and a common sign
-// would add up (outputs over 65000 tokens: 9.9e-6 off, 1.5e-6 with it).
+// would add up (outputs over 65000 tokens: 9.9e-6 off; 8.6e-7 with it, the small
+// parts first and running sums that round).
 template <typename T, int D, bool SEL>
 __global__ void __launch_bounds__(kKv4Warps<T> * 32, 1)
     kv4_attend_kernel(Kv4K a) {

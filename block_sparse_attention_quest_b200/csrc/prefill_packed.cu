@@ -31,7 +31,7 @@
 // While one tile's softmax runs, the other tile's products do.
 //
 // Measured (B200, 32/8 heads, d = 128): 32768 tokens in sequences of 1822,
-// 16384 and 14562 tokens 3630 us = 1092 TFLOP/s, tensor pipe active 62 % of
+// 16384 and 14562 tokens 3580 us = 1108 TFLOP/s, tensor pipe active 63 % of
 // the cycles, the SMs at about 1.34 GHz under the power cap (cuBLAS holds 1390
 // TFLOP/s there); 24 sequences of 0 to 1250 tokens 37 us.
 //
@@ -107,12 +107,6 @@ constexpr bool packed_ring_agrees(int slots) {
   return true;
 }
 static_assert(packed_ring_agrees(2) && packed_ring_agrees(5), "ring of K and V tiles");
-
-// The weights 2^(s sl2 - m) take the product unrounded and m, the largest
-// product, rounded: one factor 2^(its rounding) on the whole row, which from
-// |m| = 2^31 on fp32 does not hold. Rows beyond this bound round every product
-// before m is subtracted.
-constexpr float kFar = 16777216.f;
 
 __device__ __forceinline__ float ex2_fast(float x) {
   float y;
@@ -511,10 +505,10 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
         }
         l *= alpha;
         m_ref = m_new;
-        // Far rows (see kFar) come here with every tile and make s relative to
+        // Far rows (see tc::kFar) come here with every tile and make s relative to
         // their reference. (A branch of its own for them, which ordinary inputs
         // never take, costs 3 % at 32K tokens.)
-        const bool far = fabsf(m_ref) > kFar && m_ref != -INFINITY;
+        const bool far = fabsf(m_ref) > tc::kFar && m_ref != -INFINITY;
         limit = far ? -INFINITY : m_ref + 8.f;
         // (a row with no visible key yet, -inf - -inf, takes weight 0)
         nm = far || m_ref == -INFINITY ? 0.f : -m_ref;

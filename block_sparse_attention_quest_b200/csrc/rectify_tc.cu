@@ -57,12 +57,6 @@ struct RectK {
   float scale_log2;
 };
 
-// The weights 2^(s sl2 - m) take the product unrounded and m, the largest
-// product, rounded: one factor 2^(its rounding) on the whole row, which from
-// |m| = 2^31 on fp32 does not hold. Rows beyond this bound round every product
-// before m is subtracted.
-constexpr float kFar = 16777216.f;
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -342,9 +336,9 @@ __global__ void __launch_bounds__(288, 1) rectify_tc_kernel(const __grid_constan
         }
         l *= alpha;
         m_ref = m_new;
-        // Far rows (see kFar) come here with every tile and make their S
+        // Far rows (see tc::kFar) come here with every tile and make their S
         // relative to the reference.
-        const bool far = fabsf(m_ref) > kFar && m_ref != -INFINITY;
+        const bool far = fabsf(m_ref) > tc::kFar && m_ref != -INFINITY;
         limit = far ? -INFINITY : m_ref + 8.f;
         nm = far || m_ref == -INFINITY ? 0.f : -m_ref;
         if (__any_sync(0xffffffffu, far)) {

@@ -59,6 +59,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       : "memory");
 }
 
+// The softmax of both tensor-core kernels takes the weights 2^(s sl2 - m) with
+// the product unrounded and m, the row's largest product, rounded: one factor
+// 2^(its rounding) on the whole row, which from |m| = 2^31 on fp32 does not
+// hold. Rows whose reference is beyond this bound round every product before m
+// is subtracted.
+constexpr float kFar = 16777216.f;
+
 // The two products with descriptors given as their low words (address and
 // leading offset) and a shared high word, and whether to accumulate known at
 // compile time: one thread issues every product, so the instructions between

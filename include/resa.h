@@ -312,7 +312,8 @@ RESA_API int resa_rectify_varlen(const resa_dims* dims, const void* q_f, const v
  * and no other sequence. starts is read on the device only (a captured call
  * can be replayed on other lengths). out, the caches and desc must not overlap
  * q, k, v or each other (RESA_ERR_INVALID_ARG). bf16
- * only (RESA_ERR_UNSUPPORTED otherwise); any group up to 8. The workspace only
+ * only (RESA_ERR_UNSUPPORTED otherwise); any group up to 8. Each weight is
+ * rounded to bf16 where it meets v, not in its row's sum. The workspace only
  * carries the error word: resa_workspace_bytes(dims, longest, 0) suffices. */
 RESA_API int resa_prefill_packed(const resa_dims* dims, const void* q, const void* k, const void* v,
                                  const int32_t* starts, int64_t total, int64_t longest,
@@ -388,8 +389,11 @@ RESA_API int resa_evict(const resa_dims* dims, const void* k_cache, const void* 
  *      scales of token 8h + r, group g: [r][h][g][4].
  *  - Values must be finite and below 2^60 in magnitude, queries below 2^60;
  *    others give unspecified outputs in their own row (NaN and infinity are
- *    not carried through the format). softmax_scale must be below 1e17. A bf16
- *    decode call's outputs are off by up to 2^-60 besides its roundings.
+ *    not carried through the format). softmax_scale must be below 1e17.
+ *  - A bf16 decode call rounds each weight times value scale to bf16 (about
+ *    code 8) before it meets the codes. Besides its roundings its outputs are
+ *    off by up to 2^-50, and q . k by up to 2^-70 of the largest |k|. An fp32
+ *    call keeps 24 bits of every factor.
  *  - dims.dtype is the type of q, k, v, desc and out; the records are the same
  *    for both types.
  *  - lens is optional in these calls (NULL: every row has `len` tokens); with
