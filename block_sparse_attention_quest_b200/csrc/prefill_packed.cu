@@ -208,6 +208,7 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
   __shared__ __align__(8) uint64_t bar_q[NT], bar_full[C::kSlots], bar_free[3];
   __shared__ __align__(8) uint64_t bar_s[NT], bar_p[NT][2], bar_o[NT];   // [tile], P: [tile][half of the keys]
   __shared__ uint32_t tmem_base_sh;
+  __shared__ bool s_disorder;
   __shared__ int s_seq, s_block, s_tot[C::kThreads / 32];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
 
   // which sequence and which of its query blocks (the last ones, which see the
   // most keys, first): one sequence per thread, a scan of their block counts
-  if (threadIdx.x == 0) s_seq = -1;
+  if (threadIdx.x == 0) { s_seq = -1; s_disorder = false; }
   for (int b0 = 0, run = 0; b0 < a.B; b0 += C::kThreads) {
     const int b = b0 + threadIdx.x;
     int n = 0;
@@ -238,6 +239,7 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
     }
     __syncthreads();                              // (the last round's totals are read)
     if (lane == 31) s_tot[warp] = inc;
+    if (b < a.B && a.starts[b + 1] < a.starts[b]) s_disorder = true;
     __syncthreads();
     int before = run, all = run;
 #pragma unroll
@@ -256,6 +258,14 @@ __global__ void __launch_bounds__((PackedCfg<D, NT>::kThreads), (NT == 2 ? 1 : 2
   const int b = s_seq;
   if (b < 0) return;                              // more CTAs than query blocks
   const SeqBounds sb = seq_bounds(a, b);
+  // a sequence that begins below an earlier start would share tokens, and the
+  // rows of their outputs, with a sequence before it: left out
+  if (s_disorder) {
+    int top = 0;
+#pragma unroll 1
+    for (int i = 0; i < b; ++i) top = max(top, a.starts[i]);
+    if (top > sb.begin) return;
+  }
   const int q0 = s_block * QB;
   const int nq = sb.len - q0 < QB ? sb.len - q0 : QB;
   const int g = (hg << a.gs) / a.G;                  // KV head

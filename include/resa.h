@@ -305,8 +305,9 @@ RESA_API int resa_rectify_varlen(const resa_dims* dims, const void* q_f, const v
  *  - desc (or NULL): descriptors of their blocks, as resa_build_desc writes
  *    them.
  * A sequence that begins or ends outside [0, total], ends before it begins or
- * is longer than `longest` is cut to what fits and raises the
- * RESA_ERR_BAD_INDEX flag. Sequences must not share tokens. Every key and
+ * is longer than `longest` is cut to what fits; one that begins below an
+ * earlier entry of starts is left out, and those behind it may be, so that no
+ * token belongs to two sequences. Both raise the RESA_ERR_BAD_INDEX flag. Every key and
  * value should be finite: one that is not reaches every output of its own
  * sequence whose 128-token key tile holds it (also through a masked place),
  * and no other sequence. starts is read on the device only (a captured call

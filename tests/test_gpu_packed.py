@@ -325,3 +325,30 @@ def test_without_caches(resa, longest, desc):
             resa.prefill_packed(dev(q), dev(k), dev(v), torch.tensor(st, dtype=torch.int32, device="cuda"),
                                 cap + 1, None, None, d2, scale, out, ws)
         assert e.value.status == resa.RESA_ERR_CAPACITY
+
+
+@pytest.mark.parametrize("T", [2000, 2300])              # (one tile per CTA, two)
+@pytest.mark.parametrize("starts,eff", [([0, 1500, 700, 1900], {0: (0, 1500)}),
+                                        ([5, 3, 900, 10, 4, 1300, 0], {}), ([2000, 0, 100], {}),
+                                        ([0, 40, 30, 60, 100, 2000], {0: (0, 40), 3: (60, 100), 4: (100, 2000)})])
+def test_starts_out_of_order_share_no_token(resa, starts, eff, T):
+    """A sequence that begins below an earlier start is left out, so every row
+    is the one sequence's it belongs to, whichever CTA comes last."""
+    H, G, d = 1, 4, 64
+    q, k, v = rnd(1, T, H * G, d), rnd(2, T, H, d), rnd(3, T, H, d)
+    out, kc, vc, ds, ws, scale = call(resa, q, k, v, starts, 2304, T)
+    assert resa.workspace_status(ws) == resa.RESA_ERR_BAD_INDEX
+    o, inside = out.double().cpu().numpy(), np.zeros(T, bool)
+    for b in range(len(starts) - 1):
+        a, e = eff.get(b, (0, 0))
+        inside[a:e] = True
+        kn = kc[b, 0].float().cpu().numpy()
+        assert np.array_equal(kn[:e - a], k[a:e, 0]) and (kn[e - a:] == 5.0).all()
+        assert (ds[b, 0, (e - a + 15) // 16:] == 7.0).all()
+        if e > a:
+            ref = ops.packed_causal(q[a:e], k[a:e], v[a:e], [0, e - a], scale)
+            mags = ops.packed_causal(q[a:e], k[a:e], np.abs(v[a:e]), [0, e - a], scale)
+            for h in range(H * G):
+                bo = bounds(q[a:e, h].astype(np.float64), k[a:e, 0], v[a:e, 0], ref[:, h], mags[:, h], scale)
+                assert (np.abs(o[a:e, h] - ref[:, h]) <= bo).all()
+    assert (o[~inside] == 9.0).all()
